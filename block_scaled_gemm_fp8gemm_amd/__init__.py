@@ -11,6 +11,11 @@ in the library's HIP kernels; there is no fallback):
   (PyTorch supplies device memory and the current stream), allocate the outputs
   and call the ABI functions.
 
+The serving operators of ``include/fp8gemm_layers.h`` have the same two layers:
+``fp8gemm_moe_route``, ``fp8gemm_group_rows``, ``fp8gemm_moe_run``,
+``fp8gemm_moe_layer`` and ``fp8gemm_lora_run``; ``moe_route``, ``group_rows``,
+``moe_experts``, ``moe_layer`` and ``lora`` on tensors.
+
 Layouts: A is row-major [M, K]; B is column-major [K, N], passed as its
 [N, K] row-major transpose; C is row-major [M, N].  Operand codes are OCP
 e4m3fn bytes held in ``torch.uint8`` tensors.
@@ -34,10 +39,15 @@ __all__ = [
     "fp8gemm_status_string", "fp8gemm_version", "quantize", "gemm", "gemm_mxout", "gemm_qout",
     "grouped_gemm",
     "exported_symbols",
+    "SCORINGS", "fp8gemm_moe_route", "fp8gemm_group_rows_workspace_size", "fp8gemm_group_rows",
+    "fp8gemm_moe_workspace_size", "fp8gemm_moe_run", "fp8gemm_moe_layer",
+    "fp8gemm_lora_workspace_size", "fp8gemm_lora_run",
+    "moe_route", "group_rows", "moe_experts", "moe_layer", "lora", "exported_layer_symbols",
 ]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 _HEADER = os.path.join(os.path.dirname(_PKG), "include", "fp8gemm.h")
+_LAYERS_HEADER = os.path.join(os.path.dirname(_PKG), "include", "fp8gemm_layers.h")
 
 SCALE_MODES = {"tensor": 0, "rowwise": 1, "mx32": 2}
 OUT_DTYPES = {"f16": 0, "bf16": 1}
@@ -46,6 +56,8 @@ FORMATS = {"e4m3": 0, "e5m2": 1, "e2m3": 2, "e3m2": 3, "e2m1": 4}
 # bits of one code
 CODE_BITS = {"e4m3": 8, "e5m2": 8, "e2m3": 6, "e3m2": 6, "e2m1": 4}
 ACTIVATIONS = {"none": 0, "relu": 1, "gelu": 2, "silu": 3}
+
+SCORINGS = {"softmax": 0, "sigmoid": 1}
 
 # FP8GEMM_NOALLOC_SCRATCH_BYTES: the static scratch of fp8gemm_run_noalloc
 NOALLOC_SCRATCH_BYTES = 8 * 1024 * 1024 + 4096
@@ -75,6 +87,7 @@ _lib = None
 
 _i64, _i32, _sz, _p, _int = (ctypes.c_int64, ctypes.c_int32, ctypes.c_size_t, ctypes.c_void_p,
                              ctypes.c_int)
+_f32 = ctypes.c_float
 
 _SIGNATURES = {
     "fp8gemm_quantize_workspace_size": (_sz, [_i64, _i64, _int]),
@@ -102,6 +115,19 @@ _SIGNATURES = {
     "fp8gemm_run_kn_path": (_int, [_i64, _i64, _i64, _i64, _i64, _int, _int, _int]),
     "fp8gemm_run_noalloc": (_int, [_i64, _i64, _i64, _p, _i64, _int, _p, _i64, _int, _int, _p, _p,
                                    _p, _int, _p, _i64, _int, _p]),
+    "fp8gemm_moe_route": (_int, [_p, _int, _i64, _i64, _i32, _i32, _int, _int, _f32, _p, _p, _p]),
+    "fp8gemm_group_rows_workspace_size": (_sz, [_i64, _i32]),
+    "fp8gemm_group_rows": (_int, [_p, _i64, _i32, _p, _p, _p, _sz, _p]),
+    "fp8gemm_moe_workspace_size": (_sz, [_i64, _i64, _i64, _i32, _i32]),
+    "fp8gemm_moe_run": (_int, [_i64, _i64, _i64, _i32, _i32, _p, _i64, _int, _p, _p, _p, _i64,
+                               _i64, _p, _p, _i64, _i64, _p, _int, _int, _int, _p, _i64, _p, _sz,
+                               _p]),
+    "fp8gemm_moe_layer": (_int, [_i64, _i64, _i64, _i32, _i32, _p, _i64, _int, _p, _i64, _int,
+                                 _int, _int, _f32, _p, _p, _p, _i64, _i64, _p, _p, _i64, _i64, _p,
+                                 _int, _int, _int, _p, _i64, _p, _sz, _p]),
+    "fp8gemm_lora_workspace_size": (_sz, [_i64, _i64, _i32, _i32]),
+    "fp8gemm_lora_run": (_int, [_i64, _i64, _i64, _i32, _i32, _p, _i64, _p, _i64, _int, _p, _i64,
+                                _i64, _p, _i64, _i64, _p, _p, _p, _int, _p, _i64, _p, _sz, _p]),
     "fp8gemm_status_string": (ctypes.c_char_p, [_int]),
     "fp8gemm_version": (_int, []),
 }
@@ -129,7 +155,16 @@ def load_library():
 
 def exported_symbols() -> list:
     """Function names declared in include/fp8gemm.h."""
-    with open(_HEADER) as fh:
+    return _declared(_HEADER)
+
+
+def exported_layer_symbols() -> list:
+    """Function names declared in include/fp8gemm_layers.h."""
+    return _declared(_LAYERS_HEADER)
+
+
+def _declared(header) -> list:
+    with open(header) as fh:
         text = fh.read()
     return re.findall(r"^\s*(?:size_t|fp8gemm_status|const char\*|int)\s+(fp8gemm_\w+)\s*\(",
                       text, flags=re.M)
@@ -236,6 +271,63 @@ def fp8gemm_grouped_run_ex(num_groups: int, total_m: int, N: int, K: int, A: int
     _check("fp8gemm_grouped_run_ex", load_library().fp8gemm_grouped_run_ex(
         num_groups, total_m, N, K, A, lda, a_format, offsets, B, ldb, b_format, stride_b, mode,
         scale_a, scale_b, C, ldc, out_dtype, workspace, workspace_bytes, stream))
+
+
+def fp8gemm_moe_route(logits: int, dtype: int, rows: int, ldl: int, experts: int, k: int,
+                      scoring: int, renormalize: int, scale: float, ids: int, weights: int,
+                      stream: int) -> None:
+    _check("fp8gemm_moe_route", load_library().fp8gemm_moe_route(
+        logits, dtype, rows, ldl, experts, k, scoring, renormalize, scale, ids, weights, stream))
+
+
+def fp8gemm_group_rows_workspace_size(n: int, groups: int) -> int:
+    return load_library().fp8gemm_group_rows_workspace_size(n, groups)
+
+
+def fp8gemm_group_rows(ids: int, n: int, groups: int, order: int, offsets: int, workspace: int,
+                       workspace_bytes: int, stream: int) -> None:
+    _check("fp8gemm_group_rows", load_library().fp8gemm_group_rows(
+        ids, n, groups, order, offsets, workspace, workspace_bytes, stream))
+
+
+def fp8gemm_moe_workspace_size(T: int, H: int, I: int, experts: int, k: int) -> int:
+    return load_library().fp8gemm_moe_workspace_size(T, H, I, experts, k)
+
+
+def fp8gemm_moe_run(T: int, H: int, I: int, experts: int, k: int, x: int, ldx: int, dtype: int,
+                    ids: int, weights: int, w13: int, ld13: int, stride13: int, scale13: int,
+                    w2: int, ld2: int, stride2: int, scale2: int, mode: int, format: int,
+                    activation: int, out: int, ldo: int, workspace: int, workspace_bytes: int,
+                    stream: int) -> None:
+    _check("fp8gemm_moe_run", load_library().fp8gemm_moe_run(
+        T, H, I, experts, k, x, ldx, dtype, ids, weights, w13, ld13, stride13, scale13, w2, ld2,
+        stride2, scale2, mode, format, activation, out, ldo, workspace, workspace_bytes, stream))
+
+
+def fp8gemm_moe_layer(T: int, H: int, I: int, experts: int, k: int, x: int, ldx: int, dtype: int,
+                      logits: int, ldl: int, logits_dtype: int, scoring: int, renormalize: int,
+                      scale: float, ids: int, weights: int, w13: int, ld13: int, stride13: int,
+                      scale13: int, w2: int, ld2: int, stride2: int, scale2: int, mode: int,
+                      format: int, activation: int, out: int, ldo: int, workspace: int,
+                      workspace_bytes: int, stream: int) -> None:
+    _check("fp8gemm_moe_layer", load_library().fp8gemm_moe_layer(
+        T, H, I, experts, k, x, ldx, dtype, logits, ldl, logits_dtype, scoring, renormalize,
+        scale, ids, weights, w13, ld13, stride13, scale13, w2, ld2, stride2, scale2, mode, format,
+        activation, out, ldo, workspace, workspace_bytes, stream))
+
+
+def fp8gemm_lora_workspace_size(M: int, K: int, rank: int, groups: int) -> int:
+    return load_library().fp8gemm_lora_workspace_size(M, K, rank, groups)
+
+
+def fp8gemm_lora_run(M: int, N: int, K: int, rank: int, groups: int, x: int, ldx: int, base: int,
+                     ldbase: int, dtype: int, a: int, lda: int, stride_a: int, b: int, ldb: int,
+                     stride_b: int, order: int, offsets: int, scales: int, activation: int,
+                     out: int, ldo: int, workspace: int, workspace_bytes: int,
+                     stream: int) -> None:
+    _check("fp8gemm_lora_run", load_library().fp8gemm_lora_run(
+        M, N, K, rank, groups, x, ldx, base, ldbase, dtype, a, lda, stride_a, b, ldb, stride_b,
+        order, offsets, scales, activation, out, ldo, workspace, workspace_bytes, stream))
 
 
 def fp8gemm_run_noalloc(M: int, N: int, K: int, A: int, lda: int, a_format: int, B: int,
@@ -518,4 +610,244 @@ def grouped_gemm(qa, sa, offsets, qb, sb, mode: str = "rowwise", out_dtype: str 
                            _ptr(sb), _ptr(out), out.stride(0), OUT_DTYPES[out_dtype],
                            _ptr(workspace) if need else 0, workspace.numel() if need else 0,
                            _stream_handle(qa.device))
+    return out
+
+
+# ---- serving operators ----------------------------------------------------------
+@functools.lru_cache(maxsize=None)
+def _dtype_code(dtype):
+    """fp8gemm dtype of a torch activation type (None: not one)."""
+    torch = _torch()
+    return {torch.float16: 0, torch.bfloat16: 1, torch.float32: 2}.get(dtype)
+
+
+def _require(cond, message):
+    if not cond:
+        raise ValueError(message)
+
+
+def _require_like(t, name, device, dtype, shape):
+    """`t` is a CUDA tensor of this device, type and shape, unit stride in its last
+    dimension (a size of None is not checked)."""
+    if not t.is_cuda or t.device != device:
+        raise ValueError(f"{name} must be a CUDA (HIP) tensor on {device}")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must have dtype {dtype}, got {t.dtype}")
+    if t.dim() != len(shape) or any(n is not None and n != m for n, m in zip(shape, t.shape)):
+        raise ValueError(f"{name} must have shape {list(shape)}, got {list(t.shape)}")
+    if t.dim() and t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name} must have unit stride in its last dimension")
+
+
+def _row_pitch(t):
+    """Elements between the rows of a 2-D tensor.  The stride of a single row is
+    arbitrary and never used: its length, rounded up to whole 16-byte pieces, stands in."""
+    return t.stride(0) if t.shape[0] > 1 else (t.shape[1] + 7) // 8 * 8
+
+
+def _padded(rows, cols, dtype, device):
+    """[rows, cols] with a row pitch that is a multiple of 8 elements."""
+    torch = _torch()
+    pitch = (cols + 7) // 8 * 8
+    out = torch.empty((rows, pitch), dtype=dtype, device=device)
+    return out if pitch == cols else out[:, :cols]
+
+
+def _routing_outputs(T, k, device, ids, weights):
+    torch = _torch()
+    if ids is None:
+        ids = torch.empty((T, k), dtype=torch.int32, device=device)
+    else:
+        _require_like(ids, "ids", device, torch.int32, (T, k))
+        _require(ids.is_contiguous(), "ids must be contiguous")
+    if weights is None:
+        weights = torch.empty((T, k), dtype=torch.float32, device=device)
+    else:
+        _require_like(weights, "weights", device, torch.float32, (T, k))
+        _require(weights.is_contiguous(), "weights must be contiguous")
+    return ids, weights
+
+
+def _check_logits(logits):
+    _require(logits.is_cuda and logits.dim() == 2, "logits must be a 2-D CUDA (HIP) tensor")
+    code = _dtype_code(logits.dtype)
+    _require(code is not None, f"logits must be float32, float16 or bfloat16, got {logits.dtype}")
+    _require(logits.shape[1] <= 1 or logits.stride(1) == 1,
+             "logits must have unit stride in its last dimension")
+    return code
+
+
+def moe_route(logits, k: int, scoring: str = "softmax", renormalize: bool = True,
+              scale: float = 1.0, ids=None, weights=None):
+    """(ids int32 [T, k], weights float32 [T, k]): the k largest of each row of logits
+    [T, E] (float32, float16 or bfloat16), descending, equal ones by the lower expert,
+    and their softmax or sigmoid scores, divided by their sum with `renormalize`, times
+    `scale`.  Experts at -inf (or NaN) are never selected: slots left over get id -1 and
+    weight 0."""
+    code = _check_logits(logits)
+    T, E = logits.shape
+    ids, weights = _routing_outputs(T, k, logits.device, ids, weights)
+    fp8gemm_moe_route(_ptr(logits), code, T, _row_pitch(logits), E, k, SCORINGS[scoring],
+                      int(renormalize), scale, _ptr(ids), _ptr(weights),
+                      _stream_handle(logits.device))
+    return ids, weights
+
+
+def group_rows(ids, groups: int, order=None, offsets=None, workspace=None):
+    """(order int32 [n], offsets int32 [groups + 1]) of the n = ids.numel() positions of
+    a contiguous int32 tensor: order[offsets[g]:offsets[g + 1]] are the positions with
+    id g, ascending; positions whose id is outside [0, groups) follow at the end.
+
+    With moe_route's ids, order // k are the tokens sorted by expert and offsets the
+    offsets of ``grouped_gemm``; with the rows' adapter ids, the plan of ``lora``."""
+    torch = _torch()
+    _require(ids.is_cuda and ids.dtype == torch.int32 and ids.is_contiguous(),
+             "ids must be a contiguous int32 CUDA (HIP) tensor")
+    n = ids.numel()
+    if order is None:
+        order = torch.empty(n, dtype=torch.int32, device=ids.device)
+    else:
+        _require_like(order, "order", ids.device, torch.int32, (n,))
+    if offsets is None:
+        offsets = torch.empty(groups + 1, dtype=torch.int32, device=ids.device)
+    else:
+        _require_like(offsets, "offsets", ids.device, torch.int32, (groups + 1,))
+    need = fp8gemm_group_rows_workspace_size(n, groups)
+    if need and workspace is None:
+        workspace = torch.empty(need, dtype=torch.uint8, device=ids.device)
+    fp8gemm_group_rows(_ptr(ids), n, groups, _ptr(order), _ptr(offsets),
+                       _ptr(workspace) if need else 0, workspace.numel() if need else 0,
+                       _stream_handle(ids.device))
+    return order, offsets
+
+
+@functools.lru_cache(maxsize=256)
+def _moe_workspace_need(T, H, I, E, k):
+    return fp8gemm_moe_workspace_size(T, H, I, E, k)
+
+
+def _check_experts(x, qw13, sw13, qw2, sw2, mode, fmt):
+    """Shapes of a layer's tensors: (T, H, I, E)."""
+    torch = _torch()
+    _require(x.is_cuda and x.dim() == 2, "x must be a 2-D CUDA (HIP) tensor")
+    _require(x.dtype in (torch.float16, torch.bfloat16),
+             f"x must be float16 or bfloat16, got {x.dtype}")
+    _require(x.shape[1] <= 1 or x.stride(1) == 1, "x must have unit stride in its last dimension")
+    T, H = x.shape
+    _require(qw2.dim() == 3, "qw2 must be 3-D")
+    bits = CODE_BITS[fmt]
+    E, I = qw2.shape[0], qw2.shape[2] * 8 // bits
+    _require_like(qw13, "qw13", x.device, torch.uint8, (E, 2 * I, H * bits // 8))
+    _require_like(qw2, "qw2", x.device, torch.uint8, (E, H, None))
+    for name, s, n, c in (("sw13", sw13, 2 * I, H), ("sw2", sw2, H, I)):
+        if mode == "mx32":
+            _require_like(s, name, x.device, torch.uint8, (E, n, c // 32))
+        else:
+            _require(s.is_cuda and s.device == x.device and s.dtype == torch.float32 and
+                     s.numel() == (E if mode == "tensor" else E * n),
+                     f"{name} must be a float32 CUDA (HIP) tensor of "
+                     f"{E if mode == 'tensor' else E * n} scales")
+        _require(s.is_contiguous(), f"{name} must be contiguous")
+    return T, H, I, E
+
+
+def _layer_buffers(x, T, H, I, E, k, out, workspace):
+    if out is None:
+        out = _padded(T, H, x.dtype, x.device)
+    else:
+        _require_like(out, "out", x.device, x.dtype, (T, H))
+    if workspace is None:
+        workspace = gemm_workspace(x.device, max(_moe_workspace_need(T, H, I, E, k), 1))
+    return out, workspace
+
+
+def moe_experts(x, ids, weights, qw13, sw13, qw2, sw2, mode: str = "rowwise",
+                fmt: str = "e4m3", activation: str = "silu", out=None, workspace=None):
+    """out [T, H]: out_t = sum_j weights[t, j] * dq(W2_e) (act(g) * u) with g, u the two
+    halves of dq(W13_e) x_t and e = ids[t, j], for at most 128 tokens.
+
+    x: float16 or bfloat16 [T, H] (not quantised); ids int32 and weights float32 [T, k]
+    (an id outside [0, E) adds nothing); qw13 uint8 [E, 2 I, H] gate rows then up rows,
+    qw2 uint8 [E, H, I]: e4m3 codes, or e2m1 with mode "mx32" (two codes per byte);
+    sw13, sw2 as ``grouped_gemm``'s sb: float32 [E] (tensor), [E * rows] (rowwise), uint8
+    [E, rows, K / 32] (mx32).  One set of weights serves this call and ``grouped_gemm``."""
+    torch = _torch()
+    T, H, I, E = _check_experts(x, qw13, sw13, qw2, sw2, mode, fmt)
+    _require(ids.dim() == 2, "ids must be 2-D")
+    k = ids.shape[1]
+    ids, weights = _routing_outputs(T, k, x.device, ids, weights)
+    out, workspace = _layer_buffers(x, T, H, I, E, k, out, workspace)
+    fp8gemm_moe_run(T, H, I, E, k, _ptr(x), _row_pitch(x), _dtype_code(x.dtype), _ptr(ids),
+                    _ptr(weights), _ptr(qw13), qw13.stride(1), qw13.stride(0), _ptr(sw13),
+                    _ptr(qw2), qw2.stride(1), qw2.stride(0), _ptr(sw2), SCALE_MODES[mode],
+                    FORMATS[fmt], ACTIVATIONS[activation], _ptr(out), _row_pitch(out),
+                    _ptr(workspace), workspace.numel(), _stream_handle(x.device))
+    return out
+
+
+def moe_layer(x, logits, qw13, sw13, qw2, sw2, k: int, mode: str = "rowwise",
+              fmt: str = "e4m3", scoring: str = "softmax", renormalize: bool = True,
+              scale: float = 1.0, activation: str = "silu", out=None, ids=None, weights=None,
+              workspace=None):
+    """(out [T, H], ids, weights): a whole mixture-of-experts layer for at most 128 tokens,
+    ``moe_route`` on the router's logits [T, E] and ``moe_experts`` on its choice."""
+    T, H, I, E = _check_experts(x, qw13, sw13, qw2, sw2, mode, fmt)
+    code = _check_logits(logits)
+    _require(logits.device == x.device and tuple(logits.shape) == (T, E),
+             f"logits must have shape {[T, E]} on {x.device}")
+    ids, weights = _routing_outputs(T, k, x.device, ids, weights)
+    out, workspace = _layer_buffers(x, T, H, I, E, k, out, workspace)
+    fp8gemm_moe_layer(T, H, I, E, k, _ptr(x), _row_pitch(x), _dtype_code(x.dtype), _ptr(logits),
+                      _row_pitch(logits), code, SCORINGS[scoring], int(renormalize), scale,
+                      _ptr(ids), _ptr(weights), _ptr(qw13), qw13.stride(1), qw13.stride(0),
+                      _ptr(sw13), _ptr(qw2), qw2.stride(1), qw2.stride(0), _ptr(sw2),
+                      SCALE_MODES[mode], FORMATS[fmt], ACTIVATIONS[activation], _ptr(out),
+                      _row_pitch(out), _ptr(workspace), workspace.numel(),
+                      _stream_handle(x.device))
+    return out, ids, weights
+
+
+@functools.lru_cache(maxsize=256)
+def _lora_workspace_need(M, K, rank, groups):
+    return fp8gemm_lora_workspace_size(M, K, rank, groups)
+
+
+def lora(x, base, lora_a, lora_b, order, offsets, scales=None, activation: str = "none",
+         out=None, workspace=None):
+    """out [M, N] = act(base + s_g * (x A_g^T) B_g^T) for the rows of each adapter g, and
+    act(base) for rows without one.
+
+    x [M, K], base [M, N] (a projection's output), lora_a [G, rank, K], lora_b [G, N, rank]:
+    float16 or bfloat16, all the same; rank a multiple of 8 up to 128 (pad shorter adapters
+    with zeros).  order int32 [M], offsets int32 [G + 1]: the rows sorted by adapter, from
+    ``group_rows(adapter_ids, G)``; one plan serves every projection of a step.  scales:
+    float32 [G] or None.  out may be base."""
+    torch = _torch()
+    _require(x.is_cuda and x.dim() == 2, "x must be a 2-D CUDA (HIP) tensor")
+    _require(x.dtype in (torch.float16, torch.bfloat16),
+             f"x must be float16 or bfloat16, got {x.dtype}")
+    _require(x.shape[1] <= 1 or x.stride(1) == 1, "x must have unit stride in its last dimension")
+    _require(lora_a.dim() == 3 and base.dim() == 2, "lora_a must be 3-D and base 2-D")
+    M, K = x.shape
+    G, rank = lora_a.shape[:2]
+    N = base.shape[1]
+    dev, dt = x.device, x.dtype
+    _require_like(base, "base", dev, dt, (M, N))
+    _require_like(lora_a, "lora_a", dev, dt, (G, rank, K))
+    _require_like(lora_b, "lora_b", dev, dt, (G, N, rank))
+    _require_like(order, "order", dev, torch.int32, (M,))
+    _require_like(offsets, "offsets", dev, torch.int32, (G + 1,))
+    if scales is not None:
+        _require_like(scales, "scales", dev, torch.float32, (G,))
+    if out is None:
+        out = _padded(M, N, dt, dev)
+    elif out is not base:
+        _require_like(out, "out", dev, dt, (M, N))
+    if workspace is None:
+        workspace = gemm_workspace(dev, max(_lora_workspace_need(M, K, rank, G), 1))
+    fp8gemm_lora_run(M, N, K, rank, G, _ptr(x), _row_pitch(x), _ptr(base), _row_pitch(base),
+                     _dtype_code(dt), _ptr(lora_a), lora_a.stride(1), lora_a.stride(0),
+                     _ptr(lora_b), lora_b.stride(1), lora_b.stride(0), _ptr(order), _ptr(offsets),
+                     _ptr(scales), ACTIVATIONS[activation], _ptr(out), _row_pitch(out),
+                     _ptr(workspace), workspace.numel(), _stream_handle(dev))
     return out

@@ -18,7 +18,8 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libfp8gemm.so")
 
-SOURCES = ["api.cpp", "quantize.hip", "gemm.hip", "grouped.hip", "transpose.hip", "gemm_fp6.hip"]
+SOURCES = ["api.cpp", "quantize.hip", "gemm.hip", "grouped.hip", "transpose.hip", "gemm_fp6.hip",
+           "layers_api.cpp", "route.hip", "moe_few.hip", "lora.hip"]
 # gemm.hip is compiled once more per pair of operand formats other than e4m3 x e4m3
 # and once per FP8 pair for row-major B (FP8GEMM_KN), grouped.hip once more for
 # MXFP4 experts

@@ -1,0 +1,78 @@
+// Internal launch entry points of the serving operators (host side): the router,
+// the grouping of rows, the few-token mixture-of-experts layer and the low-rank
+// adapters.  Arguments are validated by layers_api.cpp before any of these runs.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace fp8gemm {
+
+constexpr int kMaxExperts = 1024;
+constexpr int kMaxTopK = 16;
+constexpr int kMoeMaxTokens = 128;
+constexpr int kLoraMaxRank = 128;
+
+// fp8gemm_out_dtype's values and the fp32 of router logits
+enum DType : int { kDtF16 = 0, kDtBF16 = 1, kDtF32 = 2 };
+
+struct RouteProblem {
+  const void* logits;
+  int dtype;
+  int rows, experts, k;
+  int64_t ld;
+  int sigmoid, renormalize;
+  float scale;
+  int32_t* ids;
+  float* weights;
+};
+hipError_t launch_route(const RouteProblem& p, hipStream_t stream);
+
+size_t group_rows_workspace_bytes(int64_t n, int groups);
+hipError_t launch_group_rows(const int32_t* ids, int n, int groups, int32_t* order,
+                             int32_t* offsets, int32_t* workspace, hipStream_t stream);
+
+struct MoeProblem {
+  int T, H, I, E, k;
+  const void* x;
+  int64_t ldx;
+  int dtype;
+  const int32_t* ids;
+  const float* weights;
+  const uint8_t* w13;
+  int64_t ld13, stride13;
+  const void* s13;
+  const uint8_t* w2;
+  int64_t ld2, stride2;
+  const void* s2;
+  int mode, format, act;
+  void* out;
+  int64_t ldo;
+  void* workspace;
+};
+size_t moe_workspace_bytes(int64_t T, int64_t H, int64_t I, int E, int k);
+hipError_t launch_moe(const MoeProblem& p, hipStream_t stream);
+
+struct LoraProblem {
+  int M, N, K, rank, groups;
+  const void* x;
+  int64_t ldx;
+  const void* base;
+  int64_t ldbase;
+  int dtype;
+  const void* a;
+  int64_t lda, stride_a;
+  const void* b;
+  int64_t ldb, stride_b;
+  const int32_t* order;
+  const int32_t* offsets;
+  const float* scales;
+  int act;
+  void* out;
+  int64_t ldo;
+  void* workspace;
+};
+size_t lora_workspace_bytes(int64_t M, int64_t K, int rank, int groups);
+hipError_t launch_lora(const LoraProblem& p, hipStream_t stream);
+
+}  // namespace fp8gemm

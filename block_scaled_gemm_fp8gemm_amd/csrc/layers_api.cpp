@@ -1,0 +1,293 @@
+// C ABI of the serving operators (include/fp8gemm_layers.h): argument validation
+// and dispatch.  As in api.cpp every check runs on the host before the first HIP
+// call, so an invalid call returns its status without touching the device.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "../../include/fp8gemm_layers.h"
+#include "launch.h"
+#include "layers.h"
+
+namespace {
+
+using fp8gemm::kMx32;
+using fp8gemm::kRowwise;
+using fp8gemm::kTensor;
+
+constexpr int64_t kMaxDim = INT32_MAX;
+// positions of fp8gemm_group_rows: its loops step by up to 1024 past the last one
+constexpr int64_t kMaxSorted = INT32_MAX - 1024;
+
+static_assert(FP8GEMM_MAX_EXPERTS == fp8gemm::kMaxExperts, "limits of the header");
+static_assert(FP8GEMM_MAX_TOP_K == fp8gemm::kMaxTopK, "limits of the header");
+static_assert(FP8GEMM_MOE_MAX_TOKENS == fp8gemm::kMoeMaxTokens, "limits of the header");
+static_assert(FP8GEMM_LORA_MAX_RANK == fp8gemm::kLoraMaxRank, "limits of the header");
+
+bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+bool valid_16bit(int d) { return d == FP8GEMM_OUT_F16 || d == FP8GEMM_OUT_BF16; }
+bool valid_act(int a) { return a >= FP8GEMM_ACT_NONE && a <= FP8GEMM_ACT_SILU; }
+
+fp8gemm_status from_hip(hipError_t e) {
+  return e == hipSuccess ? FP8GEMM_SUCCESS : FP8GEMM_ERROR_LAUNCH;
+}
+
+// Router arguments apart from the pointers of a call without rows.
+fp8gemm_status check_route(const void* logits, int dtype, int64_t rows, int64_t ldl,
+                           int32_t experts, int32_t k, int scoring, const void* ids,
+                           const void* weights) {
+  if (!(valid_16bit(dtype) || dtype == FP8GEMM_DTYPE_F32) || rows < 0 || experts < 1 || k < 1 ||
+      (scoring != FP8GEMM_SCORE_SOFTMAX && scoring != FP8GEMM_SCORE_SIGMOID))
+    return FP8GEMM_ERROR_INVALID_VALUE;
+  if (k > experts) return FP8GEMM_ERROR_INVALID_VALUE;
+  if (experts > fp8gemm::kMaxExperts || k > fp8gemm::kMaxTopK) return FP8GEMM_ERROR_NOT_SUPPORTED;
+  if (rows == 0) return FP8GEMM_SUCCESS;
+  if (!logits || !ids || !weights || ldl < experts) return FP8GEMM_ERROR_INVALID_VALUE;
+  if (rows > kMaxDim || ldl > kMaxDim) return FP8GEMM_ERROR_NOT_SUPPORTED;
+  if (!aligned(logits, dtype == FP8GEMM_DTYPE_F32 ? 4 : 2) || !aligned(ids, 4) ||
+      !aligned(weights, 4))
+    return FP8GEMM_ERROR_MISALIGNED;
+  return FP8GEMM_SUCCESS;
+}
+
+fp8gemm::RouteProblem route_problem(const void* logits, int dtype, int64_t rows, int64_t ldl,
+                                    int32_t experts, int32_t k, int scoring, int renormalize,
+                                    float scale, int32_t* ids, float* weights) {
+  fp8gemm::RouteProblem p;
+  p.logits = logits;
+  p.dtype = dtype;
+  p.rows = (int)rows;
+  p.experts = experts;
+  p.k = k;
+  p.ld = ldl;
+  p.sigmoid = scoring == FP8GEMM_SCORE_SIGMOID;
+  p.renormalize = renormalize != 0;
+  p.scale = scale;
+  p.ids = ids;
+  p.weights = weights;
+  return p;
+}
+
+// One expert matrix of rows x cols codes (bits each) per expert.
+fp8gemm_status check_expert_weights(const uint8_t* w, int64_t rows, int64_t cols, int bits,
+                                    int64_t ld, int64_t stride, const void* scale) {
+  if (!w || !scale) return FP8GEMM_ERROR_INVALID_VALUE;
+  if (ld * 8 < cols * bits || ld > kMaxDim || stride < 0) return FP8GEMM_ERROR_INVALID_VALUE;
+  if (stride / rows < ld) return FP8GEMM_ERROR_INVALID_VALUE;
+  if (!aligned(w, 16) || ld % 16 != 0 || stride % 16 != 0 || !aligned(scale, 4))
+    return FP8GEMM_ERROR_MISALIGNED;
+  return FP8GEMM_SUCCESS;
+}
+
+// Every check of fp8gemm_moe_run and fp8gemm_moe_layer; *p is filled on success.
+fp8gemm_status check_moe(int64_t T, int64_t H, int64_t I, int32_t experts, int32_t k,
+                         const void* x, int64_t ldx, int dtype, const int32_t* ids,
+                         const float* weights, const uint8_t* w13, int64_t ld13, int64_t stride13,
+                         const void* scale13, const uint8_t* w2, int64_t ld2, int64_t stride2,
+                         const void* scale2, int mode, int format, int activation, void* out,
+                         int64_t ldo, void* workspace, size_t workspace_bytes,
+                         fp8gemm::MoeProblem* p) {
+  if (T < 0 || H <= 0 || I <= 0 || experts < 1 || k < 1 || !valid_16bit(dtype) ||
+      !valid_act(activation) || (mode != kTensor && mode != kRowwise && mode != kMx32) ||
+      format < FP8GEMM_FORMAT_E4M3 || format > FP8GEMM_FORMAT_E2M1)
+    return FP8GEMM_ERROR_INVALID_VALUE;
+  const bool fp4 = format == FP8GEMM_FORMAT_E2M1;
+  if (!fp4 && format != FP8GEMM_FORMAT_E4M3) return FP8GEMM_ERROR_NOT_SUPPORTED;
+  if (fp4 && mode != kMx32) return FP8GEMM_ERROR_NOT_SUPPORTED;
+  if (T > fp8gemm::kMoeMaxTokens || experts > fp8gemm::kMaxExperts || k > fp8gemm::kMaxTopK ||
+      H > (kMaxDim >> 4) || I > (kMaxDim >> 4))
+    return FP8GEMM_ERROR_NOT_SUPPORTED;
+  const int unit = mode == kMx32 ? 32 : 16;
+  if (H % unit != 0 || I % unit != 0) return FP8GEMM_ERROR_NOT_SUPPORTED;
+  if (T == 0) return FP8GEMM_SUCCESS;
+  if (!x || !ids || !weights || !out || ldx < H || ldo < H) return FP8GEMM_ERROR_INVALID_VALUE;
+  if (ldx > kMaxDim || ldo > kMaxDim) return FP8GEMM_ERROR_NOT_SUPPORTED;
+  if (!aligned(x, 16) || !aligned(out, 16) || ldx % 8 != 0 || ldo % 8 != 0 || !aligned(ids, 4) ||
+      !aligned(weights, 4))
+    return FP8GEMM_ERROR_MISALIGNED;
+  const int bits = fp4 ? 4 : 8;
+  fp8gemm_status st = check_expert_weights(w13, 2 * I, H, bits, ld13, stride13, scale13);
+  if (st != FP8GEMM_SUCCESS) return st;
+  st = check_expert_weights(w2, H, I, bits, ld2, stride2, scale2);
+  if (st != FP8GEMM_SUCCESS) return st;
+  const size_t need = fp8gemm::moe_workspace_bytes(T, H, I, experts, k);
+  // the partial outputs are addressed with 32-bit offsets
+  if (need > (size_t)kMaxDim) return FP8GEMM_ERROR_NOT_SUPPORTED;
+  if (!workspace || workspace_bytes < need) return FP8GEMM_ERROR_WORKSPACE;
+  if (!aligned(workspace, 16)) return FP8GEMM_ERROR_MISALIGNED;
+  p->T = (int)T;
+  p->H = (int)H;
+  p->I = (int)I;
+  p->E = experts;
+  p->k = k;
+  p->x = x;
+  p->ldx = ldx;
+  p->dtype = dtype;
+  p->ids = ids;
+  p->weights = weights;
+  p->w13 = w13;
+  p->ld13 = ld13;
+  p->stride13 = stride13;
+  p->s13 = scale13;
+  p->w2 = w2;
+  p->ld2 = ld2;
+  p->stride2 = stride2;
+  p->s2 = scale2;
+  p->mode = mode;
+  p->format = format;
+  p->act = activation;
+  p->out = out;
+  p->ldo = ldo;
+  p->workspace = workspace;
+  return FP8GEMM_SUCCESS;
+}
+
+}  // namespace
+
+extern "C" {
+
+fp8gemm_status fp8gemm_moe_route(const void* logits, int dtype, int64_t rows, int64_t ldl,
+                                 int32_t experts, int32_t k, int scoring, int renormalize,
+                                 float scale, int32_t* ids, float* weights, void* stream) {
+  fp8gemm_status st = check_route(logits, dtype, rows, ldl, experts, k, scoring, ids, weights);
+  if (st != FP8GEMM_SUCCESS || rows == 0) return st;
+  return from_hip(fp8gemm::launch_route(
+      route_problem(logits, dtype, rows, ldl, experts, k, scoring, renormalize, scale, ids,
+                    weights),
+      static_cast<hipStream_t>(stream)));
+}
+
+size_t fp8gemm_group_rows_workspace_size(int64_t n, int32_t groups) {
+  if (n <= 0 || n > kMaxSorted || groups < 1 || groups > fp8gemm::kMaxExperts) return 0;
+  return fp8gemm::group_rows_workspace_bytes(n, groups);
+}
+
+fp8gemm_status fp8gemm_group_rows(const int32_t* ids, int64_t n, int32_t groups, int32_t* order,
+                                  int32_t* offsets, void* workspace, size_t workspace_bytes,
+                                  void* stream) {
+  if (n < 0 || groups < 1 || !offsets || (n > 0 && (!ids || !order)))
+    return FP8GEMM_ERROR_INVALID_VALUE;
+  if (n > kMaxSorted || groups > fp8gemm::kMaxExperts) return FP8GEMM_ERROR_NOT_SUPPORTED;
+  if (!aligned(offsets, 4) || !aligned(ids, 4) || !aligned(order, 4))
+    return FP8GEMM_ERROR_MISALIGNED;
+  const size_t need = fp8gemm_group_rows_workspace_size(n, groups);
+  if (need > 0 && (!workspace || workspace_bytes < need)) return FP8GEMM_ERROR_WORKSPACE;
+  if (need > 0 && !aligned(workspace, 4)) return FP8GEMM_ERROR_MISALIGNED;
+  return from_hip(fp8gemm::launch_group_rows(ids, (int)n, groups, order, offsets,
+                                             static_cast<int32_t*>(workspace),
+                                             static_cast<hipStream_t>(stream)));
+}
+
+size_t fp8gemm_moe_workspace_size(int64_t T, int64_t H, int64_t I, int32_t experts, int32_t k) {
+  if (T <= 0 || H <= 0 || I <= 0 || experts < 1 || k < 1 || T > fp8gemm::kMoeMaxTokens ||
+      experts > fp8gemm::kMaxExperts || k > fp8gemm::kMaxTopK || H > (kMaxDim >> 4) ||
+      I > (kMaxDim >> 4))
+    return 0;
+  return fp8gemm::moe_workspace_bytes(T, H, I, experts, k);
+}
+
+fp8gemm_status fp8gemm_moe_run(int64_t T, int64_t H, int64_t I, int32_t experts, int32_t k,
+                               const void* x, int64_t ldx, int dtype, const int32_t* ids,
+                               const float* weights, const uint8_t* w13, int64_t ld13,
+                               int64_t stride13, const void* scale13, const uint8_t* w2,
+                               int64_t ld2, int64_t stride2, const void* scale2, int mode,
+                               int format, int activation, void* out, int64_t ldo,
+                               void* workspace, size_t workspace_bytes, void* stream) {
+  fp8gemm::MoeProblem p;
+  fp8gemm_status st = check_moe(T, H, I, experts, k, x, ldx, dtype, ids, weights, w13, ld13,
+                                stride13, scale13, w2, ld2, stride2, scale2, mode, format,
+                                activation, out, ldo, workspace, workspace_bytes, &p);
+  if (st != FP8GEMM_SUCCESS || T == 0) return st;
+  return from_hip(fp8gemm::launch_moe(p, static_cast<hipStream_t>(stream)));
+}
+
+fp8gemm_status fp8gemm_moe_layer(int64_t T, int64_t H, int64_t I, int32_t experts, int32_t k,
+                                 const void* x, int64_t ldx, int dtype, const void* logits,
+                                 int64_t ldl, int logits_dtype, int scoring, int renormalize,
+                                 float scale, int32_t* ids, float* weights, const uint8_t* w13,
+                                 int64_t ld13, int64_t stride13, const void* scale13,
+                                 const uint8_t* w2, int64_t ld2, int64_t stride2,
+                                 const void* scale2, int mode, int format, int activation,
+                                 void* out, int64_t ldo, void* workspace, size_t workspace_bytes,
+                                 void* stream) {
+  fp8gemm_status st =
+      check_route(logits, logits_dtype, T, ldl, experts, k, scoring, ids, weights);
+  if (st != FP8GEMM_SUCCESS) return st;
+  fp8gemm::MoeProblem p;
+  st = check_moe(T, H, I, experts, k, x, ldx, dtype, ids, weights, w13, ld13, stride13, scale13,
+                 w2, ld2, stride2, scale2, mode, format, activation, out, ldo, workspace,
+                 workspace_bytes, &p);
+  if (st != FP8GEMM_SUCCESS || T == 0) return st;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  hipError_t e = fp8gemm::launch_route(
+      route_problem(logits, logits_dtype, T, ldl, experts, k, scoring, renormalize, scale, ids,
+                    weights), s);
+  if (e != hipSuccess) return FP8GEMM_ERROR_LAUNCH;
+  return from_hip(fp8gemm::launch_moe(p, s));
+}
+
+size_t fp8gemm_lora_workspace_size(int64_t M, int64_t K, int32_t rank, int32_t groups) {
+  if (M <= 0 || M > kMaxDim || K <= 0 || K > kMaxDim || rank < 1 ||
+      rank > fp8gemm::kLoraMaxRank || groups < 1 || groups > fp8gemm::kMaxExperts)
+    return 0;
+  return fp8gemm::lora_workspace_bytes(M, K, rank, groups);
+}
+
+fp8gemm_status fp8gemm_lora_run(int64_t M, int64_t N, int64_t K, int32_t rank, int32_t groups,
+                                const void* x, int64_t ldx, const void* base, int64_t ldbase,
+                                int dtype, const void* a, int64_t lda, int64_t stride_a,
+                                const void* b, int64_t ldb, int64_t stride_b,
+                                const int32_t* order, const int32_t* offsets,
+                                const float* scales, int activation, void* out, int64_t ldo,
+                                void* workspace, size_t workspace_bytes, void* stream) {
+  if (M < 0 || N < 0 || K <= 0 || rank < 1 || groups < 1 || !valid_16bit(dtype) ||
+      !valid_act(activation))
+    return FP8GEMM_ERROR_INVALID_VALUE;
+  if (rank > fp8gemm::kLoraMaxRank || groups > fp8gemm::kMaxExperts || K % 8 != 0 || rank % 8 != 0)
+    return FP8GEMM_ERROR_NOT_SUPPORTED;
+  if (M == 0 || N == 0) return FP8GEMM_SUCCESS;
+  if (!x || !base || !a || !b || !order || !offsets || !out) return FP8GEMM_ERROR_INVALID_VALUE;
+  if (ldx < K || ldbase < N || ldo < N || lda < K || ldb < rank || stride_a < 0 || stride_b < 0 ||
+      stride_a / rank < lda || stride_b / N < ldb)
+    return FP8GEMM_ERROR_INVALID_VALUE;
+  if (M > kMaxDim || N > kMaxDim || K > kMaxDim || ldx > kMaxDim || ldbase > kMaxDim ||
+      ldo > kMaxDim || lda > kMaxDim || ldb > kMaxDim)
+    return FP8GEMM_ERROR_NOT_SUPPORTED;
+  // row tiles by column tiles of 64 and more: keep the grid below 2^31
+  if ((M / 16 + groups + 1) * ((N + 63) / 64) > kMaxDim) return FP8GEMM_ERROR_NOT_SUPPORTED;
+  if (!aligned(x, 16) || !aligned(base, 16) || !aligned(a, 16) || !aligned(b, 16) ||
+      !aligned(out, 16) || !aligned(order, 4) || !aligned(offsets, 4) || !aligned(scales, 4))
+    return FP8GEMM_ERROR_MISALIGNED;
+  if (ldx % 8 != 0 || ldbase % 8 != 0 || ldo % 8 != 0 || lda % 8 != 0 || ldb % 8 != 0 ||
+      stride_a % 8 != 0 || stride_b % 8 != 0)
+    return FP8GEMM_ERROR_MISALIGNED;
+  const size_t need = fp8gemm_lora_workspace_size(M, K, rank, groups);
+  if (!workspace || workspace_bytes < need) return FP8GEMM_ERROR_WORKSPACE;
+  if (!aligned(workspace, 16)) return FP8GEMM_ERROR_MISALIGNED;
+  fp8gemm::LoraProblem p;
+  p.M = (int)M;
+  p.N = (int)N;
+  p.K = (int)K;
+  p.rank = rank;
+  p.groups = groups;
+  p.x = x;
+  p.ldx = ldx;
+  p.base = base;
+  p.ldbase = ldbase;
+  p.dtype = dtype;
+  p.a = a;
+  p.lda = lda;
+  p.stride_a = stride_a;
+  p.b = b;
+  p.ldb = ldb;
+  p.stride_b = stride_b;
+  p.order = order;
+  p.offsets = offsets;
+  p.scales = scales;
+  p.act = activation;
+  p.out = out;
+  p.ldo = ldo;
+  p.workspace = workspace;
+  return from_hip(fp8gemm::launch_lora(p, static_cast<hipStream_t>(stream)));
+}
+
+}  // extern "C"

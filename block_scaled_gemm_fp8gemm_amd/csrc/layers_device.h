@@ -1,0 +1,57 @@
+// Device helpers shared by the few-token layer kernels: vector types, the weight
+// codes' conversion, activations, 16-bit splits and written-through partials.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "device_utils.h"
+#include "launch.h"
+#include "layers.h"
+
+namespace fp8gemm {
+
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+
+// Activations of fp32 values; exp(-v) overflows to infinity for v < -88, which
+// gives the limit -0.
+__device__ __forceinline__ float layer_activate(float v, int act) {
+  if (act == kActRelu) return fmaxf(v, 0.0f);
+  if (act == kActGelu) return 0.5f * v * (1.0f + erff(v * 0.70710678118654752f));
+  if (act == kActSilu) return v / (1.0f + __expf(-v));
+  return v;
+}
+
+// v = hi + lo to 16 significant bits (relative error at most 2^-17 unless lo
+// underflows): the operand of two bf16 matrix products in place of one fp32 one.
+__device__ __forceinline__ void split_bf16(float v, __bf16& hi, __bf16& lo) {
+  hi = (__bf16)v;
+  lo = (__bf16)(v - (float)hi);
+}
+
+// The raw-buffer cache policy of relaxed agent-scope atomics (SC1): stores are
+// written through to, and loads read from, the memory level that all XCDs share,
+// so an exchange between workgroups needs no cache flush, only completed stores.
+constexpr int kShared = 16;
+
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t shared_buffer(void* base, uint32_t bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(base, (short)0, (int)bytes, 0x00020000);
+}
+
+// Four fp32 values rounded to a 16-bit type, one 8-byte store.
+template <typename OutT>
+__device__ __forceinline__ void store4(OutT* to, const float (&v)[4]) {
+  OutT o[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) o[i] = to_out<OutT>(v[i]);
+  uint2 w;
+  __builtin_memcpy(&w, o, 8);
+  *reinterpret_cast<uint2*>(to) = w;
+}
+
+}  // namespace fp8gemm

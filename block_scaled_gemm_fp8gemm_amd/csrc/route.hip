@@ -1,0 +1,373 @@
+// The router of a mixture-of-experts layer and the grouping of rows for gfx950.
+//
+// Router: the k largest of E logits of a token, in descending order, equal ones by
+// the lower expert first, and their softmax or sigmoid weights.  A token is held by
+// L lanes (L a power of two, S consecutive experts per lane), so selection and sums
+// stay in registers: logits become unsigned keys that order like the floats, each
+// of the k rounds takes the largest key by butterfly shuffles and the lowest lane
+// that holds it (experts are numbered lane by lane, so that lane holds the lowest
+// index).  Selection compares logits, never rounded probabilities.
+//
+// Grouping: a stable counting sort by group id.  Ranks come from wave ballots (the
+// lanes below with the same id), so no atomic's order reaches the result.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "device_utils.h"
+#include "launch.h"
+#include "layers.h"
+
+namespace fp8gemm {
+namespace {
+
+// ---------------------------------------------------------------------------
+// Router
+// ---------------------------------------------------------------------------
+constexpr int kRouteThreads = 256;
+
+__device__ __forceinline__ float load_logit(const void* row, int e, int dtype) {
+  if (dtype == kDtF32) return static_cast<const float*>(row)[e];
+  if (dtype == kDtF16) return (float)static_cast<const _Float16*>(row)[e];
+  return (float)static_cast<const __bf16*>(row)[e];
+}
+
+// 0 for masked experts (-inf, NaN); otherwise larger for larger logits, -0 as +0.
+__device__ __forceinline__ uint32_t logit_key(float v) {
+  v += 0.0f;
+  if (!(v > -__builtin_inff())) return 0u;
+  const uint32_t u = __float_as_uint(v);
+  return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+}
+__device__ __forceinline__ float key_logit(uint32_t key) {
+  return __uint_as_float((key & 0x80000000u) ? (key & 0x7fffffffu) : ~key);
+}
+
+// L lanes per token, S experts per lane: L * S >= experts, k <= L.
+template <int L, int S>
+__global__ __launch_bounds__(kRouteThreads) void route_kernel(RouteProblem p) {
+  constexpr int kPerBlock = kRouteThreads / L;
+  const int lane = (int)threadIdx.x % L;            // within the token's lanes
+  const int wlane = (int)threadIdx.x % 64;
+  const int token = (int)blockIdx.x * kPerBlock + (int)threadIdx.x / L;
+  const bool live = token < p.rows;
+  const size_t elem = p.dtype == kDtF32 ? 4 : 2;
+  const void* row = static_cast<const uint8_t*>(p.logits) + (size_t)(live ? token : 0) * p.ld * elem;
+
+  uint32_t key[S];
+#pragma unroll
+  for (int s = 0; s < S; ++s) {
+    const int e = lane * S + s;
+    key[s] = (live && e < p.experts) ? logit_key(load_logit(row, e, p.dtype)) : 0u;
+  }
+  const uint64_t group = (L == 64 ? ~0ull : ((1ull << L) - 1)) << (wlane / L * L);
+
+  uint32_t best = 0;
+  int at = 0;
+  auto local_best = [&] {
+    best = 0;
+    at = 0;
+#pragma unroll
+    for (int s = 0; s < S; ++s)
+      if (key[s] > best) {
+        best = key[s];
+        at = s;
+      }
+  };
+  local_best();
+  uint32_t top = 0, mine = 0;                       // the row's largest key; slot `lane`'s key
+  int my_id = -1;
+  float rest = 0.0f;                                // sum of exp(l - max) over all experts
+  for (int j = 0; j < p.k; ++j) {
+    uint32_t m = best;
+#pragma unroll
+    for (int off = L / 2; off >= 1; off >>= 1) {
+      const uint32_t o = (uint32_t)__shfl_xor((int)m, off, 64);
+      m = o > m ? o : m;
+    }
+    const uint64_t holders = __ballot(best == m) & group;
+    const int winner = __builtin_ctzll(holders);    // never empty: a lane of the group holds m
+    const int e = __shfl((lane * S + at), winner, 64);
+    if (j == 0) {
+      top = m;
+      // p = exp(l - max) / sum: every term at most 1; l == max covers infinity
+      if (!p.sigmoid && !p.renormalize) {
+        const float mx = key_logit(top);
+#pragma unroll
+        for (int s = 0; s < S; ++s)
+          if (key[s] != 0) rest += key[s] == top ? 1.0f : expf(key_logit(key[s]) - mx);
+#pragma unroll
+        for (int off = L / 2; off >= 1; off >>= 1) rest += __shfl_xor(rest, off, 64);
+      }
+    }
+    if (lane == j) {
+      mine = m;
+      my_id = m != 0 ? e : -1;
+    }
+    if (wlane == winner && m != 0) {
+#pragma unroll
+      for (int s = 0; s < S; ++s)
+        if (s == at) key[s] = 0;
+      local_best();
+    }
+  }
+  // slot `lane`: its score and, to renormalise, the sum over the selected
+  float w = 0.0f;
+  if (mine != 0) {
+    const float l = key_logit(mine), mx = key_logit(top);
+    // where every sigmoid underflows, 1 / (1 + e^-l) = e^l to fp32 and the ratios
+    // are those of the softmax
+    if (p.sigmoid && !(p.renormalize && mx < -60.0f)) w = 1.0f / (1.0f + expf(-l));
+    else w = mine == top ? 1.0f : expf(l - mx);
+  }
+  float sum = w;
+#pragma unroll
+  for (int off = L / 2; off >= 1; off >>= 1) sum += __shfl_xor(sum, off, 64);
+  if (p.renormalize) w = sum > 0.0f ? w / sum : 0.0f;
+  else if (!p.sigmoid) w = rest > 0.0f ? w / rest : 0.0f;
+  if (live && lane < p.k) {
+    p.ids[(int64_t)token * p.k + lane] = my_id;
+    p.weights[(int64_t)token * p.k + lane] = w * p.scale;
+  }
+}
+
+template <int L, int S>
+hipError_t launch_route_as(const RouteProblem& p, hipStream_t stream) {
+  constexpr int kPerBlock = kRouteThreads / L;
+  hipLaunchKernelGGL((route_kernel<L, S>), dim3((unsigned)((p.rows + kPerBlock - 1) / kPerBlock)),
+                     dim3(kRouteThreads), 0, stream, p);
+  return hipGetLastError();
+}
+
+// ---------------------------------------------------------------------------
+// Grouping
+// ---------------------------------------------------------------------------
+constexpr int kSortThreads = 1024;
+constexpr int kSortWaves = kSortThreads / 64;
+constexpr int kMaxBlocks = 256;               // blocks of the three-kernel form
+constexpr int kOneBlock = 16384;              // positions that one workgroup sorts alone
+
+// Group of position i: [0, groups), or `groups` for an id that names none.
+__device__ __forceinline__ int group_of(const int32_t* ids, int i, int groups) {
+  const int g = ids[i];
+  return (unsigned)g < (unsigned)groups ? g : groups;
+}
+
+// The lanes of `active` whose g equals this lane's (bits: enough for every g).
+__device__ __forceinline__ uint64_t same_group(int g, uint64_t active, int bits) {
+  uint64_t same = active;
+  for (int b = 0; b < bits; ++b) {
+    const uint64_t set = __ballot((g >> b) & 1);
+    same &= ((g >> b) & 1) ? set : ~set;
+  }
+  return same;
+}
+
+// Exclusive prefix sums over the workgroup's threads, and the total (all threads).
+__device__ __forceinline__ int exclusive_scan(int v, int* scratch, int* total) {
+  const int lane = (int)threadIdx.x % 64, wave = (int)threadIdx.x / 64;
+  int x = v;
+#pragma unroll
+  for (int off = 1; off < 64; off <<= 1) {
+    const int o = __shfl_up(x, off, 64);
+    if (lane >= off) x += o;
+  }
+  if (lane == 63) scratch[wave] = x;
+  __syncthreads();
+  int before = 0, all = 0;
+  for (int w = 0; w < (int)blockDim.x / 64; ++w) {
+    const int s = scratch[w];
+    before += w < wave ? s : 0;
+    all += s;
+  }
+  *total = all;
+  return before + x - v;
+}
+
+// Places the positions [first, last) of this wave: next[g] is the place of the
+// next position of group g (LDS, this wave's own).
+__device__ __forceinline__ void place(const int32_t* ids, int first, int last, int groups,
+                                      int bits, int* next, int32_t* order) {
+  const int lane = (int)threadIdx.x % 64;
+  for (int i0 = first; i0 < last; i0 += 64) {
+    const int i = i0 + lane;
+    const bool live = i < last;
+    const int g = live ? group_of(ids, i, groups) : groups;
+    const uint64_t same = same_group(g, __ballot(live), bits);
+    const int rank = __popcll(same & ((1ull << lane) - 1));
+    int at = 0;
+    if (live) at = next[g] + rank;
+    // every lane has read its group's place before the group's last lane moves it on
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    if (live && (same >> lane) == 1ull) next[g] = at + 1;
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    if (live) order[at] = i;
+  }
+}
+
+// One workgroup: histogram per wave, prefix sums over waves and groups, placement.
+__global__ __launch_bounds__(kSortThreads) void sort_one_kernel(const int32_t* ids, int n,
+                                                               int groups, int bits, int chunk,
+                                                               int32_t* order, int32_t* offsets) {
+  __shared__ int next[kSortWaves][kMaxExperts + 1];
+  __shared__ int scratch[kSortWaves];
+  const int t = (int)threadIdx.x, wave = t / 64, lane = t % 64;
+  for (int w = 0; w < kSortWaves; ++w)
+    for (int g = t; g <= groups; g += kSortThreads) next[w][g] = 0;
+  __syncthreads();
+  const int first = wave * chunk < n ? wave * chunk : n;
+  const int last = first + chunk < n ? first + chunk : n;
+  for (int i = first + lane; i < last; i += 64) atomicAdd(&next[wave][group_of(ids, i, groups)], 1);
+  __syncthreads();
+  int count = 0;
+  if (t < groups)
+    for (int w = 0; w < kSortWaves; ++w) {
+      const int c = next[w][t];
+      next[w][t] = count;                       // places before this wave's, within the group
+      count += c;
+    }
+  int valid;
+  const int base = exclusive_scan(t < groups ? count : 0, scratch, &valid);
+  if (t < groups) {
+    offsets[t] = base;
+    for (int w = 0; w < kSortWaves; ++w) next[w][t] += base;
+  }
+  if (t == 0) {
+    offsets[groups] = valid;
+    int at = valid;                             // positions of no group follow
+    for (int w = 0; w < kSortWaves; ++w) {
+      const int c = next[w][groups];
+      next[w][groups] = at;
+      at += c;
+    }
+  }
+  __syncthreads();
+  place(ids, first, last, groups, bits, next[wave], order);
+}
+
+// Many positions, three kernels: counts[g][block], their prefix sums over the
+// blocks, then the placement.  Blocks are contiguous runs of positions.
+__global__ __launch_bounds__(kSortThreads) void sort_count_kernel(const int32_t* ids, int n,
+                                                                  int groups, int span,
+                                                                  int32_t* counts) {
+  __shared__ int hist[kMaxExperts + 1];
+  for (int g = (int)threadIdx.x; g <= groups; g += kSortThreads) hist[g] = 0;
+  __syncthreads();
+  const int64_t first = (int64_t)blockIdx.x * span;
+  const int64_t last = first + span < n ? first + span : n;
+  for (int64_t i = first + threadIdx.x; i < last; i += kSortThreads)
+    atomicAdd(&hist[group_of(ids, (int)i, groups)], 1);
+  __syncthreads();
+  for (int g = (int)threadIdx.x; g <= groups; g += kSortThreads)
+    counts[(int64_t)g * gridDim.x + blockIdx.x] = hist[g];
+}
+
+// One wave per group: exclusive prefix sums of its row of counts, and the total.
+__global__ __launch_bounds__(64) void sort_scan_kernel(int32_t* counts, int blocks,
+                                                       int32_t* totals) {
+  int32_t* row = counts + (int64_t)blockIdx.x * blocks;
+  const int lane = (int)threadIdx.x;
+  int before = 0;
+  for (int b0 = 0; b0 < blocks; b0 += 64) {
+    const int b = b0 + lane;
+    const int v = b < blocks ? row[b] : 0;
+    int x = v;
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1) {
+      const int o = __shfl_up(x, off, 64);
+      if (lane >= off) x += o;
+    }
+    if (b < blocks) row[b] = before + x - v;
+    before += __shfl(x, 63, 64);
+  }
+  if (lane == 0) totals[blockIdx.x] = before;
+}
+
+__global__ __launch_bounds__(kSortThreads) void sort_place_kernel(
+    const int32_t* ids, int n, int groups, int bits, int span, int chunk, const int32_t* counts,
+    const int32_t* totals, int32_t* order, int32_t* offsets) {
+  __shared__ int next[kSortWaves][kMaxExperts + 1];
+  __shared__ int scratch[kSortWaves];
+  const int t = (int)threadIdx.x, wave = t / 64, lane = t % 64;
+  for (int w = 0; w < kSortWaves; ++w)
+    for (int g = t; g <= groups; g += kSortThreads) next[w][g] = 0;
+  __syncthreads();
+  const int64_t block0 = (int64_t)blockIdx.x * span;
+  const int64_t block1 = block0 + span < n ? block0 + span : n;
+  const int64_t f = block0 + (int64_t)wave * chunk;
+  const int first = (int)(f < block1 ? f : block1);
+  const int last = (int)(f + chunk < block1 ? f + chunk : block1);
+  for (int i = first + lane; i < last; i += 64) atomicAdd(&next[wave][group_of(ids, i, groups)], 1);
+  __syncthreads();
+  int valid;
+  const int total = t < groups ? totals[t] : 0;
+  const int base = exclusive_scan(total, scratch, &valid);
+  if (blockIdx.x == 0 && t < groups) offsets[t] = base;
+  if (blockIdx.x == 0 && t == 0) offsets[groups] = valid;
+  auto spread = [&](int g, int at) {
+    for (int w = 0; w < kSortWaves; ++w) {
+      const int c = next[w][g];
+      next[w][g] = at;
+      at += c;
+    }
+  };
+  if (t < groups) spread(t, base + counts[(int64_t)t * gridDim.x + blockIdx.x]);
+  if (t == kSortThreads - 1)
+    spread(groups, valid + counts[(int64_t)groups * gridDim.x + blockIdx.x]);
+  __syncthreads();
+  place(ids, first, last, groups, bits, next[wave], order);
+}
+
+__global__ void sort_none_kernel(int32_t* offsets, int groups) {
+  for (int g = (int)threadIdx.x; g <= groups; g += (int)blockDim.x) offsets[g] = 0;
+}
+
+int sort_blocks(int64_t n) {
+  const int64_t b = (n + 4095) / 4096;
+  return (int)(b < kMaxBlocks ? b : kMaxBlocks);
+}
+
+}  // namespace
+
+hipError_t launch_route(const RouteProblem& p, hipStream_t stream) {
+  if (p.experts <= 8) return launch_route_as<8, 1>(p, stream);
+  if (p.experts <= 16) return launch_route_as<16, 1>(p, stream);
+  if (p.experts <= 32) return launch_route_as<32, 1>(p, stream);
+  if (p.experts <= 64) return launch_route_as<64, 1>(p, stream);
+  if (p.experts <= 128) return launch_route_as<64, 2>(p, stream);
+  if (p.experts <= 256) return launch_route_as<64, 4>(p, stream);
+  if (p.experts <= 512) return launch_route_as<64, 8>(p, stream);
+  return launch_route_as<64, 16>(p, stream);
+}
+
+size_t group_rows_workspace_bytes(int64_t n, int groups) {
+  if (n <= kOneBlock) return 0;
+  return sizeof(int32_t) * ((size_t)(groups + 1) * sort_blocks(n) + (size_t)(groups + 1));
+}
+
+hipError_t launch_group_rows(const int32_t* ids, int n, int groups, int32_t* order,
+                             int32_t* offsets, int32_t* workspace, hipStream_t stream) {
+  int bits = 1;
+  while ((1 << bits) <= groups) ++bits;             // ids 0 .. groups
+  auto up64 = [](int64_t v) { return (int)((v + 63) / 64 * 64); };
+  if (n == 0) {
+    hipLaunchKernelGGL(sort_none_kernel, dim3(1), dim3(256), 0, stream, offsets, groups);
+  } else if (n <= kOneBlock) {
+    const int chunk = up64((n + kSortWaves - 1) / kSortWaves);
+    hipLaunchKernelGGL(sort_one_kernel, dim3(1), dim3(kSortThreads), 0, stream, ids, n, groups,
+                       bits, chunk, order, offsets);
+  } else {
+    const int blocks = sort_blocks(n);
+    const int chunk = up64(((int64_t)n + (int64_t)blocks * kSortWaves - 1) / (blocks * kSortWaves));
+    const int span = chunk * kSortWaves;            // blocks past the end have no positions
+    int32_t* totals = workspace + (size_t)(groups + 1) * blocks;
+    hipLaunchKernelGGL(sort_count_kernel, dim3(blocks), dim3(kSortThreads), 0, stream, ids, n,
+                       groups, span, workspace);
+    hipLaunchKernelGGL(sort_scan_kernel, dim3(groups + 1), dim3(64), 0, stream, workspace, blocks,
+                       totals);
+    hipLaunchKernelGGL(sort_place_kernel, dim3(blocks), dim3(kSortThreads), 0, stream, ids, n,
+                       groups, bits, span, chunk, workspace, totals, order, offsets);
+  }
+  return hipGetLastError();
+}
+
+}  // namespace fp8gemm

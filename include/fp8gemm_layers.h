@@ -1,0 +1,161 @@
+/*
+ * fp8gemm_layers.h - serving operators around the scaled GEMMs of fp8gemm.h.
+ *
+ *   fp8gemm_moe_route   router logits -> the k best experts of each token and their weights
+ *   fp8gemm_group_rows  positions sorted by group id, with the groups' offsets (the row order
+ *                       and offsets of fp8gemm_grouped_run, and the plan of fp8gemm_lora_run)
+ *   fp8gemm_moe_run     the experts of a mixture-of-experts layer for a few tokens: 16-bit
+ *                       activations, FP8 / FP4 expert weights read once, two kernels
+ *   fp8gemm_moe_layer   the same from the router's logits
+ *   fp8gemm_lora_run    low-rank adapters of many requests added beside a projection's output
+ *
+ * The conventions are those of fp8gemm.h: device pointers, host sizes, a hipStream_t passed as
+ * void*, asynchronous calls that validate on the host first, allocate nothing, never
+ * synchronise and keep no state; the same status codes, scale modes, formats and activations.
+ * No call records a memset node and no result depends on the order in which workgroups run, so
+ * the calls can be captured in a HIP graph and repeat bit for bit.  Row pitches (ld) and expert
+ * strides count elements of the tensor (bytes for code tensors).
+ */
+#ifndef FP8GEMM_LAYERS_H_
+#define FP8GEMM_LAYERS_H_
+
+#include "fp8gemm.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+/* Element types of activations: FP8GEMM_OUT_F16, FP8GEMM_OUT_BF16, and for router logits also */
+#define FP8GEMM_DTYPE_F32 2
+
+typedef enum fp8gemm_scoring {
+  FP8GEMM_SCORE_SOFTMAX = 0, /* p_e = exp(l_e) / sum over all experts of exp(l) */
+  FP8GEMM_SCORE_SIGMOID = 1  /* p_e = 1 / (1 + exp(-l_e))                       */
+} fp8gemm_scoring;
+
+#define FP8GEMM_MAX_EXPERTS 1024   /* experts of a router or layer, groups of fp8gemm_group_rows */
+#define FP8GEMM_MAX_TOP_K 16
+#define FP8GEMM_MOE_MAX_TOKENS 128
+#define FP8GEMM_LORA_MAX_RANK 128
+
+/* ------------------------------------------------------------------------- */
+/* Router: for each row of logits [rows][experts] the k largest, in descending   */
+/* order, equal ones by the lower index first, and their weights                 */
+/*   w_j = scale * p_j                              (renormalize == 0)           */
+/*   w_j = scale * p_j / sum over the selected of p (renormalize != 0).          */
+/* Selection compares the logits themselves (both scores grow with the logit), so */
+/* it does not depend on rounding.  A logit of -inf or NaN masks its expert: it is */
+/* never selected and has p = 0; with fewer than k experts left the last slots get */
+/* id -1 and weight 0.  Experts at +inf share the probability among themselves.    */
+/*   logits : device, dtype F32 / F16 / BF16, row pitch ldl >= experts elements,   */
+/*            aligned to its element.                                             */
+/*   ids    : device int32 [rows][k]; weights: device float [rows][k], 4-byte      */
+/*            aligned.                                                            */
+/* 1 <= k <= min(experts, FP8GEMM_MAX_TOP_K), experts <= FP8GEMM_MAX_EXPERTS (more  */
+/* of either: NOT_SUPPORTED; k > experts: INVALID_VALUE).                          */
+/* Sums and exponentials are fp32.                                                */
+/* ------------------------------------------------------------------------- */
+fp8gemm_status fp8gemm_moe_route(const void* logits, int dtype, int64_t rows, int64_t ldl,
+                                 int32_t experts, int32_t k, int scoring, int renormalize,
+                                 float scale, int32_t* ids, float* weights, void* stream);
+
+/* ------------------------------------------------------------------------- */
+/* Positions 0 .. n-1 sorted by group: order[offsets[g] .. offsets[g+1]) are the   */
+/* positions p with ids[p] == g, ascending (a stable counting sort).  Positions    */
+/* whose id is outside [0, groups) belong to no group and follow, ascending, in     */
+/* order[offsets[groups] .. n).                                                   */
+/*   ids, order: device int32 [n]; offsets: device int32 [groups + 1]; 4-byte       */
+/*   aligned; order may not overlap ids.  0 <= n <= 2^31 - 1025, 1 <= groups <=     */
+/*   FP8GEMM_MAX_EXPERTS.                                                         */
+/*   workspace: fp8gemm_group_rows_workspace_size() bytes, 4-byte aligned (0: NULL   */
+/*   allowed); scratch.                                                           */
+/* ------------------------------------------------------------------------- */
+size_t fp8gemm_group_rows_workspace_size(int64_t n, int32_t groups);
+
+fp8gemm_status fp8gemm_group_rows(const int32_t* ids, int64_t n, int32_t groups, int32_t* order,
+                                  int32_t* offsets, void* workspace, size_t workspace_bytes,
+                                  void* stream);
+
+/* ------------------------------------------------------------------------- */
+/* The experts of a mixture-of-experts layer for a few tokens:                    */
+/*   g = dq(W13_e)[0 .. I) x_t,  u = dq(W13_e)[I .. 2I) x_t,                       */
+/*   out_t = cast( sum_j weights[t][j] * dq(W2_e) (act(g) * u) ),  e = ids[t][j].  */
+/* The activations stay in their 16-bit type (x is not quantised), act(g)*u is     */
+/* carried with 16 significant bits, sums are fp32, and out is rounded once.      */
+/*   x   : device [T][H], dtype F16 / BF16, pitch ldx >= H, out the same type,     */
+/*         pitch ldo >= H; pitches multiples of 8, 16-byte aligned.                */
+/*   ids : device int32 [T][k], weights: device float [T][k].  A slot whose id is  */
+/*         outside [0, experts) adds nothing; a token with no slot left gets zeros. */
+/*   W13 : expert e's gate rows then up rows, 2I rows of H codes, at               */
+/*         w13 + e*stride13, pitch ld13 bytes; W2: H rows of I codes at            */
+/*         w2 + e*stride2, pitch ld2.  Both E4M3 (any scale mode) or E2M1 (MX32,    */
+/*         two codes per byte).  Layouts of codes and scales as the B operand of    */
+/*         fp8gemm_grouped_run (scale13: [E], [E*2I] or [E][2I][H/32]; scale2: [E],  */
+/*         [E*H] or [E][H][I/32]), so one set of weights serves both calls.  An MX   */
+/*         code of 0 (2^-127) is read as zero.                                    */
+/*   H, I: multiples of 16 (32 with MX32) and H of 8.                             */
+/* 0 <= T <= FP8GEMM_MOE_MAX_TOKENS (more: NOT_SUPPORTED; the grouped GEMM serves    */
+/* longer batches), 1 <= k <= FP8GEMM_MAX_TOP_K, experts <= FP8GEMM_MAX_EXPERTS.      */
+/*   workspace: fp8gemm_moe_workspace_size() bytes, 16-byte aligned; scratch whose   */
+/*         first 4 KiB stay untouched (a workspace of fp8gemm_run may be shared by    */
+/*         calls that run one after another).                                       */
+/* ------------------------------------------------------------------------- */
+size_t fp8gemm_moe_workspace_size(int64_t T, int64_t H, int64_t I, int32_t experts, int32_t k);
+
+fp8gemm_status fp8gemm_moe_run(int64_t T, int64_t H, int64_t I, int32_t experts, int32_t k,
+                               const void* x, int64_t ldx, int dtype, const int32_t* ids,
+                               const float* weights, const uint8_t* w13, int64_t ld13,
+                               int64_t stride13, const void* scale13, const uint8_t* w2,
+                               int64_t ld2, int64_t stride2, const void* scale2, int mode,
+                               int format, int activation, void* out, int64_t ldo,
+                               void* workspace, size_t workspace_bytes, void* stream);
+
+/* The whole layer: fp8gemm_moe_route on logits [T][experts] (pitch ldl, type
+   logits_dtype) and fp8gemm_moe_run with its ids and weights, which are outputs here. */
+fp8gemm_status fp8gemm_moe_layer(int64_t T, int64_t H, int64_t I, int32_t experts, int32_t k,
+                                 const void* x, int64_t ldx, int dtype, const void* logits,
+                                 int64_t ldl, int logits_dtype, int scoring, int renormalize,
+                                 float scale, int32_t* ids, float* weights, const uint8_t* w13,
+                                 int64_t ld13, int64_t stride13, const void* scale13,
+                                 const uint8_t* w2, int64_t ld2, int64_t stride2,
+                                 const void* scale2, int mode, int format, int activation,
+                                 void* out, int64_t ldo, void* workspace, size_t workspace_bytes,
+                                 void* stream);
+
+/* ------------------------------------------------------------------------- */
+/* Low-rank adapters of many requests beside a shared projection:                 */
+/*   out_m = cast( act( base_m + s_g * (x_m A_g^T) B_g^T ) )                       */
+/* for the rows m = order[p], offsets[g] <= p < offsets[g+1], of each group g, and   */
+/*   out_m = cast( act( base_m ) )   for the rows order[p], p >= offsets[groups].    */
+/*   x   : device [M][K], base and out: device [M][N]; all dtype F16 / BF16; base is  */
+/*         the projection's output (fp8gemm_run's C); out may be base itself, and may  */
+/*         overlap neither it otherwise nor x.                                      */
+/*   A   : group g's [rank][K] rows at a + g*stride_a, pitch lda; B: its [N][rank] rows */
+/*         at b + g*stride_b, pitch ldb; the same dtype.                              */
+/*   scales: device float [groups], or NULL (1).                                     */
+/*   order : device int32 [M], a permutation of the rows; offsets: device int32          */
+/*         [groups + 1], non-decreasing from 0 (fp8gemm_group_rows on the rows' adapter    */
+/*         ids, -1 for none; one plan serves every projection of a step).  Entries that     */
+/*         break these rules touch nothing outside the tensors, but leave out unspecified.   */
+/*   K, rank: multiples of 8; rank <= FP8GEMM_LORA_MAX_RANK; N any.  Pitches and strides       */
+/*         multiples of 8 elements, bases 16-byte aligned.                                  */
+/* x A^T is kept in fp32 between the two products, sums are fp32, out is rounded once.         */
+/*   workspace: fp8gemm_lora_workspace_size() bytes, 16-byte aligned; scratch whose first      */
+/*         4 KiB stay untouched.                                                           */
+/* 0 <= M, N < 2^31, 1 <= groups <= FP8GEMM_MAX_EXPERTS.                                     */
+/* ------------------------------------------------------------------------- */
+size_t fp8gemm_lora_workspace_size(int64_t M, int64_t K, int32_t rank, int32_t groups);
+
+fp8gemm_status fp8gemm_lora_run(int64_t M, int64_t N, int64_t K, int32_t rank, int32_t groups,
+                                const void* x, int64_t ldx, const void* base, int64_t ldbase,
+                                int dtype, const void* a, int64_t lda, int64_t stride_a,
+                                const void* b, int64_t ldb, int64_t stride_b,
+                                const int32_t* order, const int32_t* offsets,
+                                const float* scales, int activation, void* out, int64_t ldo,
+                                void* workspace, size_t workspace_bytes, void* stream);
+
+#ifdef __cplusplus
+}
+#endif
+
+#endif /* FP8GEMM_LAYERS_H_ */
