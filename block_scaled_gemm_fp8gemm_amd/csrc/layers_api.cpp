@@ -15,6 +15,8 @@ using fp8gemm::kRowwise;
 using fp8gemm::kTensor;
 
 constexpr int64_t kMaxDim = INT32_MAX;
+// H and I of a layer: row scales are addressed with 32-bit byte offsets
+constexpr int64_t kMaxInner = int64_t(1) << 27;
 // positions of fp8gemm_group_rows: its loops step by up to 1024 past the last one
 constexpr int64_t kMaxSorted = INT32_MAX - 1024;
 
@@ -73,6 +75,8 @@ fp8gemm_status check_expert_weights(const uint8_t* w, int64_t rows, int64_t cols
   if (!w || !scale) return FP8GEMM_ERROR_INVALID_VALUE;
   if (ld * 8 < cols * bits || ld > kMaxDim || stride < 0) return FP8GEMM_ERROR_INVALID_VALUE;
   if (stride / rows < ld) return FP8GEMM_ERROR_INVALID_VALUE;
+  // 16 rows are addressed with 32-bit offsets
+  if (ld >= (int64_t(1) << 27)) return FP8GEMM_ERROR_NOT_SUPPORTED;
   if (!aligned(w, 16) || ld % 16 != 0 || stride % 16 != 0 || !aligned(scale, 4))
     return FP8GEMM_ERROR_MISALIGNED;
   return FP8GEMM_SUCCESS;
@@ -94,7 +98,7 @@ fp8gemm_status check_moe(int64_t T, int64_t H, int64_t I, int32_t experts, int32
   if (!fp4 && format != FP8GEMM_FORMAT_E4M3) return FP8GEMM_ERROR_NOT_SUPPORTED;
   if (fp4 && mode != kMx32) return FP8GEMM_ERROR_NOT_SUPPORTED;
   if (T > fp8gemm::kMoeMaxTokens || experts > fp8gemm::kMaxExperts || k > fp8gemm::kMaxTopK ||
-      H > (kMaxDim >> 4) || I > (kMaxDim >> 4))
+      H >= kMaxInner || I >= kMaxInner)
     return FP8GEMM_ERROR_NOT_SUPPORTED;
   const int unit = mode == kMx32 ? 32 : 16;
   if (H % unit != 0 || I % unit != 0) return FP8GEMM_ERROR_NOT_SUPPORTED;
@@ -110,8 +114,14 @@ fp8gemm_status check_moe(int64_t T, int64_t H, int64_t I, int32_t experts, int32
   st = check_expert_weights(w2, H, I, bits, ld2, stride2, scale2);
   if (st != FP8GEMM_SUCCESS) return st;
   const size_t need = fp8gemm::moe_workspace_bytes(T, H, I, experts, k);
-  // the partial outputs are addressed with 32-bit offsets
-  if (need > (size_t)kMaxDim) return FP8GEMM_ERROR_NOT_SUPPORTED;
+  // x and the workspace are addressed with 32-bit offsets, larger ones mark lanes without
+  // a column
+  constexpr int64_t kMaxSpan = 0x70000000;
+  if (need > (size_t)kMaxSpan || ((T - 1) * ldx + H) * 2 > kMaxSpan)
+    return FP8GEMM_ERROR_NOT_SUPPORTED;
+  // the groups of rows of all experts in use are counted through (8: parts of K)
+  if (T * k * ((I + 15) / 16) > kMaxDim || T * k * ((H + 31) / 32) * 8 > kMaxDim)
+    return FP8GEMM_ERROR_NOT_SUPPORTED;
   if (!workspace || workspace_bytes < need) return FP8GEMM_ERROR_WORKSPACE;
   if (!aligned(workspace, 16)) return FP8GEMM_ERROR_MISALIGNED;
   p->T = (int)T;
@@ -179,8 +189,8 @@ fp8gemm_status fp8gemm_group_rows(const int32_t* ids, int64_t n, int32_t groups,
 
 size_t fp8gemm_moe_workspace_size(int64_t T, int64_t H, int64_t I, int32_t experts, int32_t k) {
   if (T <= 0 || H <= 0 || I <= 0 || experts < 1 || k < 1 || T > fp8gemm::kMoeMaxTokens ||
-      experts > fp8gemm::kMaxExperts || k > fp8gemm::kMaxTopK || H > (kMaxDim >> 4) ||
-      I > (kMaxDim >> 4))
+      experts > fp8gemm::kMaxExperts || k > fp8gemm::kMaxTopK || H >= kMaxInner ||
+      I >= kMaxInner)
     return 0;
   return fp8gemm::moe_workspace_bytes(T, H, I, experts, k);
 }

@@ -5,14 +5,16 @@
 // With few tokens every product is bound by reading the selected experts' codes
 // once from HBM, so the two kernels stream weight rows and keep everything else out
 // of the way:
-//   * 16-row tiles of codes go from global memory straight into registers, 16 bytes
-//     per lane, and are converted there to the 16-bit type of the activations (one
-//     instruction per two codes; MX scales are powers of two and are folded in
-//     exactly).  They are the first operand of v_mfma_f32_16x16x32; up to 16 tokens
-//     are its columns, so one token or sixteen cost the same weight traffic.
-//   * The eight waves of a workgroup split K: together they read whole weight rows
-//     at once, 16 consecutive rows of the matrix, which DRAM serves like one
-//     contiguous block.  Their sums meet in LDS.
+//   * Weight rows are copied to LDS in whole 128-byte lines (direct-to-LDS loads with the
+//     non-temporal hint), 16 rows by CH bytes at a time, into a ring of two slots that
+//     each wave keeps for itself: a wave waits for its own copies only, and the copies of
+//     the next chunk, of the next unit too, are in flight over the products of this one.
+//   * From there 16 bytes per lane are converted to the 16-bit type of the activations
+//     (one instruction per two codes; MX scales are powers of two and are folded in
+//     exactly).  They are the first operand of v_mfma_f32_16x16x32; up to 16 tokens are
+//     its columns, so one token or sixteen cost the same weight traffic.
+//   * The waves of a workgroup take a row's chunks in turn: together they read W * CH
+//     consecutive bytes of each row at once.  Their sums meet in LDS.
 //   * A lane's 16 bytes are consecutive K, so the K order inside a matrix
 //     instruction is permuted; the activations are loaded in the same order.
 //   * The intermediate h is kept as two bf16 (hi + lo, 16 significant bits) and
@@ -31,11 +33,8 @@
 namespace fp8gemm {
 namespace {
 
-constexpr int kThreads = 512;
-constexpr int kWaves = kThreads / 64;
 constexpr int kMaxPairs = kMoeMaxTokens * kMaxTopK;
 constexpr int kStep = 64;            // bytes of a weight row per 16-byte load of four lane groups
-constexpr int kChunk = 256;          // bytes of a weight row loaded at once: whole cache lines
 
 // Form of the activation operand: bf16 or f16 as given; f16 split into two bf16 on
 // the way (MX scales need bf16's exponent range); pairs of bf16 as the up kernel
@@ -46,28 +45,32 @@ enum XForm { kXBf16, kXF16, kXF16Split, kXPair };
 // Experts in use and their (token, slot) pairs
 // ---------------------------------------------------------------------------
 struct Lists {
-  int count[kMaxExperts];            // then: next free place of an expert's pairs
-  int expert[kMaxExperts];           // experts in use, ascending
-  int start[kMaxExperts + 1];        // their pairs: list[start[a] .. start[a+1])
+  uint16_t expert[kMaxExperts];      // experts in use, ascending
+  uint16_t start[kMaxExperts + 2];   // their pairs: list[start[a] .. start[a+1])
+  uint16_t block[kMaxExperts + 2];   // their column blocks, counted through
   uint16_t list[kMaxPairs];          // pair = token * k + slot
   int used;
 };
 
-__device__ __forceinline__ void build_lists(Lists& l, const MoeProblem& p) {
+// cols: pairs of a column block; count: kMaxExperts words of LDS, scratch.
+__device__ __forceinline__ void build_lists(Lists& l, int* count, const MoeProblem& p, int cols) {
+  const int kThreads = (int)blockDim.x;
   const int t = (int)threadIdx.x, pairs = p.T * p.k;
-  for (int e = t; e < p.E; e += kThreads) l.count[e] = 0;
+  for (int e = t; e < p.E; e += kThreads) count[e] = 0;
   __syncthreads();
   for (int i = t; i < pairs; i += kThreads) {
     const unsigned e = (unsigned)p.ids[i];
-    if (e < (unsigned)p.E) atomicAdd(&l.count[e], 1);
+    if (e < (unsigned)p.E) atomicAdd(&count[e], 1);
   }
   __syncthreads();
   if (t < 64) {
-    int used = 0, placed = 0;
+    int used = 0, placed = 0, blocks = 0;
     for (int e0 = 0; e0 < p.E; e0 += 64) {
       const int e = e0 + t;
-      const int c = e < p.E ? l.count[e] : 0;
-      int x = c;
+      const int c = e < p.E ? count[e] : 0;
+      // pairs (at most 2048 in all) and column blocks in one scan
+      int x = c | (((c + cols - 1) / cols) << 16);
+      const int own = x;
 #pragma unroll
       for (int off = 1; off < 64; off <<= 1) {
         const int o = __shfl_up(x, off, 64);
@@ -76,27 +79,121 @@ __device__ __forceinline__ void build_lists(Lists& l, const MoeProblem& p) {
       const uint64_t in_use = __ballot(c > 0);
       if (c > 0) {
         const int a = used + __popcll(in_use & ((1ull << t) - 1));
-        l.expert[a] = e;
-        l.start[a] = placed + x - c;
-        l.count[e] = placed + x - c;
+        l.expert[a] = (uint16_t)e;
+        l.start[a] = (uint16_t)(placed + ((x - own) & 0xffff));
+        l.block[a] = (uint16_t)(blocks + ((x - own) >> 16));
+        count[e] = placed + ((x - own) & 0xffff);    // next free place
       }
       used += __popcll(in_use);
-      placed += __shfl(x, 63, 64);
+      const int all = __shfl(x, 63, 64);
+      placed += all & 0xffff;
+      blocks += all >> 16;
     }
     if (t == 0) {
-      l.start[used] = placed;
+      l.start[used] = (uint16_t)placed;
+      l.block[used] = (uint16_t)blocks;
       l.used = used;
     }
-  }
-  __syncthreads();
-  // the order within an expert may differ between workgroups; a pair's values do
-  // not depend on the column it takes
-  for (int i = t; i < pairs; i += kThreads) {
-    const unsigned e = (unsigned)p.ids[i];
-    if (e < (unsigned)p.E) l.list[atomicAdd(&l.count[e], 1)] = (uint16_t)i;
+    // The pairs of an expert in ascending order, the same in every workgroup, since
+    // column blocks are dealt to different ones: 64 pairs at a time, a pair's rank
+    // among them is the number of lower lanes with its expert.
+    int bits = 0;
+    while ((1 << bits) < p.E) ++bits;
+    for (int i0 = 0; i0 < pairs; i0 += 64) {
+      const int i = i0 + t;
+      const int e = i < pairs ? p.ids[i] : -1;
+      const bool live = (unsigned)e < (unsigned)p.E;
+      uint64_t same = __ballot(live);
+      for (int b = 0; b < bits; ++b) {
+        const uint64_t set = __ballot((e >> b) & 1);
+        same &= ((e >> b) & 1) ? set : ~set;
+      }
+      int at = 0;
+      if (live) at = count[e] + __popcll(same & ((1ull << t) - 1));
+      // every lane has read its expert's place before the last of them moves it on
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      if (live && (same >> t) == 1ull) count[e] = at + 1;
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      if (live) l.list[at] = (uint16_t)i;
+    }
   }
   __syncthreads();
 }
+
+// The work.  The rows of an expert (and of a part of K) are cut into tiles of NP groups of
+// 32 rows; a unit is a tile and one column block.  The workgroups take the units in turn,
+// so neighbouring tiles are read at the same time all over the chip, and the units of
+// one tile's column blocks, eight numbers apart, run together on one XCD: its L2 then
+// serves all but one of them.  What is left after the last whole round is cut finer, into
+// pieces of 1, 2 or NP groups, whichever leaves the busiest workgroup the least.
+struct Unit {
+  int e, part, group, groups;        // expert, part of K, first group, how many (0: none)
+  int from, last;                    // pairs list[from .. last): the columns
+  bool alone;                        // the tile's only column block
+};
+
+template <int NP>
+struct Schedule {
+  int groups, parts, cols;           // of an expert's rows; parts of K; columns of a block
+  int tiles, whole, piece;           // of an expert's rows; units taken whole; groups of a piece
+  int items;                         // units taken whole and pieces
+
+  __device__ __forceinline__ Schedule(const Lists& l, int groups_, int parts_, int cols_)
+      : groups(groups_), parts(parts_), cols(cols_) {
+    const int grid = (int)gridDim.x;
+    tiles = (groups + NP - 1) / NP;
+    const int units = (int)l.block[l.used] * parts * tiles;
+    const int rest = units % grid;
+    whole = units - rest;
+    piece = NP;
+    int least = rest ? NP : 0;
+#pragma unroll
+    for (int m = NP / 2; m >= 1; m /= 2) {
+      const int load = (rest * (NP / m) + grid - 1) / grid * m;
+      if (load < least) {
+        least = load;
+        piece = m;
+      }
+    }
+    items = __builtin_amdgcn_readfirstlane(whole + rest * (NP / piece));
+    whole = __builtin_amdgcn_readfirstlane(whole);
+    piece = __builtin_amdgcn_readfirstlane(piece);
+  }
+
+  // Item i (UNIFORM: the same in every lane).  a: a place in the list of active experts not
+  // past its expert's, moved there.
+  template <bool UNIFORM = true>
+  __device__ __forceinline__ Unit at(const Lists& l, int i, int& a) const {
+    auto value = [](int v) { return UNIFORM ? __builtin_amdgcn_readfirstlane(v) : v; };
+    int unit = i, first = 0, most = NP;
+    if (i >= whole) {
+      const int per = NP / piece, q = i - whole;
+      unit = whole + q / per;
+      first = q % per * piece;
+      most = piece;
+    }
+    while (unit >= value(l.block[a + 1]) * parts * tiles) ++a;
+    const int b0 = value(l.block[a]);
+    const int blocks = value(l.block[a + 1]) - b0;
+    const int local = unit - b0 * parts * tiles;       // part by part, eight tiles by eight
+    Unit w;
+    w.part = local / (blocks * tiles);
+    const int in_part = local - w.part * blocks * tiles;
+    const int first8 = in_part / (8 * blocks) * 8;
+    const int run = tiles - first8 < 8 ? tiles - first8 : 8;
+    const int in_run = in_part - first8 * blocks;
+    const int block = in_run / run;
+    w.e = value(l.expert[a]);
+    w.group = (first8 + in_run - block * run) * NP + first;
+    w.groups = groups - w.group < most ? groups - w.group : most;
+    w.groups = w.groups < 0 ? 0 : w.groups;
+    w.from = value(l.start[a]) + block * cols;
+    const int last = value(l.start[a + 1]);
+    w.last = w.from + cols < last ? w.from + cols : last;
+    w.alone = blocks == 1;
+    return w;
+  }
+};
 
 // ---------------------------------------------------------------------------
 // 16-row tiles of weight rows times columns of activations over a range of K
@@ -137,119 +234,169 @@ __device__ __forceinline__ u32x4 decode8(const u32x4& w, int m, float scale) {
   return r;
 }
 
-// One lane's view of a matrix of weight rows: its row's codes (from its lane
-// group's first 16 bytes on) and, with MX, its row's scale codes.
-struct WeightRow {
-  const uint8_t* codes;
-  const uint8_t* scales;
+// What a wave reads for one unit: RT sub-tiles of 16 rows; sub-tile r starts at codes[r],
+// a wave-uniform address.
+constexpr int kNoColumn = 0x70000000;  // past the end of every activation buffer: reads zero
+
+template <int RT, int NT>
+struct Source {
+  const uint8_t* codes[RT];
+  const uint8_t* scales[RT];          // MX codes of this lane's row (row lane % 16)
+  const float* row_scale;             // row-wise: scales from a wave-uniform address, and the
+  int row_scale_at[(RT + 3) / 4];     // byte offsets of those that this lane copies
+  int col[NT];                        // byte offset of this lane's column of activations, from
+                                      // its lane group's first element on
+  int c0, c1;                         // chunks of K
+  bool alone;                         // no other unit reads these rows
+  int groups;                         // sub-tiles 2 * groups and more are not read
 };
 
-template <int FMT>
-struct ScaleWords {                   // the scale codes of one chunk of a row
-  uint32_t w[FMT == kE2M1 ? 4 : 2];
+// The registers of one chunk: the activations and the MX scale codes.
+template <int FMT, bool MX, int X, int RT, int NT, int CH>
+struct Side {
+  static constexpr int kSteps = CH / kStep;
+  static constexpr int kF = kFrags<FMT>;
+  static constexpr int kXFrag = X == kXPair ? 32 : 16;      // bytes of 8 activations
+  static constexpr int kCodes = FMT == kE2M1 ? CH / 16 : CH / 32;   // MX scale codes of a row
+  uint32_t sc[MX ? RT : 1][(kCodes + 3) / 4];
+  u32x4 x[kSteps][NT][kF][kXFrag / 16];
+  int c;                                                    // which chunk
+  int groups;
 };
 
-template <int FMT, bool MX, int RT>
-__device__ __forceinline__ void load_chunk(const WeightRow (&row)[RT], int c, int bytes, int grp,
-                                           u32x4 (&w)[kChunk / kStep][RT],
-                                           ScaleWords<FMT> (&sc)[RT]) {
-  constexpr int kCodes = FMT == kE2M1 ? 16 : 8;      // scale codes of a chunk
-  const bool full = (c + 1) * kChunk <= bytes;
+// 16 bytes per lane from a buffer to LDS (lane i to dst + 16 i).  Rows that one unit alone
+// reads take the non-temporal hint (7.0 against 6.3 TB/s in a plain stream of tiles).
+constexpr int kNonTemporal = 2;
+template <int AUX>
+__device__ __forceinline__ void copy_to_lds(__amdgpu_buffer_rsrc_t rs, uint8_t* dst, int voff,
+                                            int soff) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (__attribute__((address_space(3))) void*)dst, 16,
+                                           voff, soff, 0, AUX);
+}
+
+// Place of 16-byte piece q of row r in a slot (rows of CH bytes): the pieces of a row
+// are permuted so that the 16 rows of an operand read spread over all LDS banks.
+template <int CH>
+__device__ __forceinline__ int swizzle(int r) {
+  return CH == 256 ? r & 15 : (r >> 1) & 7;
+}
+
+template <int W, int FMT, int MODE, int X, int RT, int NT, int CH>
+struct Stream {
+  static constexpr bool MX = MODE == kMx32;
+  using S = Side<FMT, MX, X, RT, NT, CH>;
+  static constexpr int kSlot = RT * 16 * CH;          // bytes of a chunk's codes
+  static constexpr int kRowsPer = 1024 / CH;          // rows that one copy covers
+  static constexpr int kCopies = 2 * 16 / kRowsPer;   // copies of a group's rows
+  uint8_t* ring;                                      // this wave's two slots
+  float (*row_scale)[RT < 4 ? 64 : 16 * RT];          // row-wise: the rows' scales, by unit
+  __amdgpu_buffer_rsrc_t x;                           // the activations
+  int lane, grp, bytes;                               // bytes: of a weight row
+  int64_t ld;
+
+  // Starts the loads of chunk c: the side registers, then the codes to slot `slot`.
+  __device__ __forceinline__ void issue(const Source<RT, NT>& src, int c, S& side, int slot) const {
+    const bool full = (c + 1) * CH <= bytes;
+    side.c = c;
+    side.groups = src.groups;
+    constexpr int kXStep = 4 * S::kF * S::kXFrag;     // of a step: four lane groups
 #pragma unroll
-  for (int s = 0; s < kChunk / kStep; ++s)
+    for (int s = 0; s < S::kSteps; ++s) {
+      const int off = c * CH + s * kStep;
+      const bool past = !full && off + grp * 16 >= bytes;
 #pragma unroll
-    for (int r = 0; r < RT; ++r) {
-      const int off = c * kChunk + s * kStep;
-      w[s][r] = u32x4{0, 0, 0, 0};
-      if (full || off + grp * 16 < bytes)
-        w[s][r] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(row[r].codes + off));
+      for (int n = 0; n < NT; ++n) {
+        const int at = past ? kNoColumn : src.col[n];
+#pragma unroll
+        for (int m = 0; m < S::kF; ++m)
+#pragma unroll
+          for (int h = 0; h < S::kXFrag / 16; ++h)
+            side.x[s][n][m][h] = __builtin_bit_cast(
+                u32x4, __builtin_amdgcn_raw_buffer_load_b128(
+                           x, at + m * S::kXFrag + h * 16, off / kStep * kXStep, 0));
+      }
     }
-  if constexpr (MX) {
-    const int blocks = FMT == kE2M1 ? bytes / 16 : bytes / 32;
+    if constexpr (MX) {
+      const int blocks = FMT == kE2M1 ? bytes / 16 : bytes / 32;
 #pragma unroll
-    for (int r = 0; r < RT; ++r) {
-      if (full) {
-        __builtin_memcpy(sc[r].w, row[r].scales + c * kCodes, kCodes);
-      } else {
+      for (int r = 0; r < RT; ++r) {
+        if (full) {
+          __builtin_memcpy(side.sc[r], src.scales[r] + c * S::kCodes, S::kCodes);
+        } else {
 #pragma unroll
-        for (int i = 0; i < kCodes / 4; ++i) {
-          sc[r].w[i] = 0;
+          for (int i = 0; i < (S::kCodes + 3) / 4; ++i) {
+            side.sc[r][i] = 0;
 #pragma unroll
-          for (int b = 0; b < 4; ++b) {
-            const int at = c * kCodes + 4 * i + b;
-            if (at < blocks) sc[r].w[i] |= (uint32_t)row[r].scales[at] << (8 * b);
+            for (int b = 0; b < 4; ++b) {
+              const int at = c * S::kCodes + 4 * i + b;
+              if (4 * i + b < S::kCodes && at < blocks)
+                side.sc[r][i] |= (uint32_t)src.scales[r][at] << (8 * b);
+            }
           }
         }
       }
     }
+    uint8_t* to = ring + slot * kSlot;
+#pragma unroll
+    for (int r = 0; r < RT; ++r) {
+      if (r / 2 >= src.groups) break;
+      const __amdgpu_buffer_rsrc_t rs =
+          __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(src.codes[r]), (short)0,
+                                            0x7fffffff, 0x00020000);
+#pragma unroll
+      for (int i = 0; i < 16 / kRowsPer; ++i) {
+        const int row = i * kRowsPer + lane / (CH / 16);
+        int piece = ((lane % (CH / 16)) ^ swizzle<CH>(row)) * 16;
+        // past the row's end: its last piece; the product takes zeros instead
+        if (!full && c * CH + piece >= bytes) piece = bytes - 16 - c * CH;
+        uint8_t* dst = to + (r * 16 + i * kRowsPer) * CH;
+        if (src.alone) copy_to_lds<kNonTemporal>(rs, dst, row * (int)ld + piece, c * CH);
+        else copy_to_lds<0>(rs, dst, row * (int)ld + piece, c * CH);
+      }
+    }
   }
-}
 
-// Scale of this lane group's block in step s of a chunk.  E4M3: a step is 64
-// codes, two blocks, two lane groups each; E2M1: 128 codes, one block per group.
-template <int FMT>
-__device__ __forceinline__ float step_scale(const ScaleWords<FMT>& sc, int s, int grp) {
-  const uint32_t code = FMT == kE2M1 ? (sc.w[s] >> (8 * grp)) & 0xffu
-                                     : (sc.w[s >> 1] >> (16 * (s & 1) + 8 * (grp >> 1))) & 0xffu;
-  return __uint_as_float(code << 23);
-}
+  // Scale of this lane group's block in step s.  E4M3: a step is 64 codes, two
+  // blocks, two lane groups each; E2M1: 128 codes, one block per lane group.
+  __device__ __forceinline__ float scale(const S& side, int r, int s) const {
+    const uint32_t code = FMT == kE2M1
+                              ? (side.sc[r][s] >> (8 * grp)) & 0xffu
+                              : (side.sc[r][s >> 1] >> (16 * (s & 1) + 8 * (grp >> 1))) & 0xffu;
+    return __uint_as_float(code << 23);
+  }
 
-// acc[r][n] += rows of tile r times columns of tile n over the chunks [c0, c1).
-// col[n]: this lane's column from its lane group's first element on, null: no
-// column (reads nothing, counts as zero).
-template <int FMT, bool MX, int X, int RT, int NT>
-__device__ __forceinline__ void stream_rows(const WeightRow (&row)[RT],
-                                            const uint8_t* const (&col)[NT], int bytes, int c0,
-                                            int c1, int grp, f32x4 (&acc)[RT][NT]) {
-  constexpr int kF = kFrags<FMT>;
-  constexpr int kXFrag = X == kXPair ? 32 : 16;      // bytes of 8 activations
-  constexpr int kXStep = 4 * kF * kXFrag;            // of a step: four lane groups
-  u32x4 w[2][kChunk / kStep][RT];
-  ScaleWords<FMT> sc[2][RT];
-  if (c0 >= c1) return;
-  load_chunk<FMT, MX, RT>(row, c0, bytes, grp, w[0], sc[0]);
-  auto step = [&](int c, int now) __attribute__((always_inline)) {
-    if (c + 1 < c1) load_chunk<FMT, MX, RT>(row, c + 1, bytes, grp, w[now ^ 1], sc[now ^ 1]);
-    const bool full = (c + 1) * kChunk <= bytes;
+  __device__ __forceinline__ void multiply(const S& side, int slot, f32x4 (&acc)[RT][NT]) const {
+    const uint8_t* from = ring + slot * kSlot + (lane & 15) * CH;
+    const bool full = (side.c + 1) * CH <= bytes;
 #pragma unroll
-    for (int s = 0; s < kChunk / kStep; ++s) {
-      const int off = c * kChunk + s * kStep;
-      const bool live = full || off + grp * 16 < bytes;
-      u32x4 xv[NT][kF][kXFrag / 16];
+    for (int s = 0; s < S::kSteps; ++s) {
+      u32x4 w[RT];
 #pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        const u32x4* from =
-            reinterpret_cast<const u32x4*>(col[n] + (int64_t)(off / kStep) * kXStep);
-#pragma unroll
-        for (int m = 0; m < kF; ++m)
-#pragma unroll
-          for (int h = 0; h < kXFrag / 16; ++h) xv[n][m][h] = u32x4{0, 0, 0, 0};
-        if (col[n] && live) {
-#pragma unroll
-          for (int m = 0; m < kF; ++m)
-#pragma unroll
-            for (int h = 0; h < kXFrag / 16; ++h) xv[n][m][h] = from[m * (kXFrag / 16) + h];
-        }
+      for (int r = 0; r < RT; ++r) {
+        w[r] = *reinterpret_cast<const u32x4*>(from + r * 16 * CH +
+                                               ((4 * s + grp) ^ swizzle<CH>(lane & 15)) * 16);
+        if (!full && side.c * CH + s * kStep + grp * 16 >= bytes) w[r] = u32x4{0, 0, 0, 0};
       }
 #pragma unroll
-      for (int m = 0; m < kF; ++m) {
+      for (int m = 0; m < S::kF; ++m) {
         u32x4 a[RT];
 #pragma unroll
         for (int r = 0; r < RT; ++r)
-          a[r] = decode8<FMT, X>(w[now][s][r], m, MX ? step_scale<FMT>(sc[now][r], s, grp) : 1.0f);
+          a[r] = decode8<FMT, X>(w[r], m, MX ? scale(side, r, s) : 1.0f);
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
           if constexpr (X == kXF16) {
 #pragma unroll
             for (int r = 0; r < RT; ++r)
               acc[r][n] = __builtin_amdgcn_mfma_f32_16x16x32_f16(
-                  __builtin_bit_cast(f16x8, a[r]), __builtin_bit_cast(f16x8, xv[n][m][0]),
+                  __builtin_bit_cast(f16x8, a[r]), __builtin_bit_cast(f16x8, side.x[s][n][m][0]),
                   acc[r][n], 0, 0, 0);
           } else {
-            bf16x8 hi = __builtin_bit_cast(bf16x8, xv[n][m][0]), lo{};
-            if constexpr (X == kXPair) lo = __builtin_bit_cast(bf16x8, xv[n][m][kXFrag / 16 - 1]);
+            bf16x8 hi = __builtin_bit_cast(bf16x8, side.x[s][n][m][0]), lo{};
+            if constexpr (X == kXPair)
+              lo = __builtin_bit_cast(bf16x8, side.x[s][n][m][S::kXFrag / 16 - 1]);
             if constexpr (X == kXF16Split) {
-              const f16x8 f = __builtin_bit_cast(f16x8, xv[n][m][0]);
+              const f16x8 f = __builtin_bit_cast(f16x8, side.x[s][n][m][0]);
 #pragma unroll
               for (int i = 0; i < 8; ++i) {
                 __bf16 a1, a2;
@@ -270,47 +417,158 @@ __device__ __forceinline__ void stream_rows(const WeightRow (&row)[RT],
         }
       }
     }
-  };
-  int c = c0;
-  for (; c + 1 < c1; c += 2) {
-    step(c, 0);
-    step(c + 1, 1);
   }
-  if (c < c1) step(c, 0);
-}
 
-// Sums of the eight waves: waves store their accumulators of one column tile,
-// [wave][column][row], rows padded by four against bank conflicts.
-template <int RT>
-struct Partials {
-  float v[2][kWaves][16][16 * RT + 4];
+  // Waits until at most the copies of `groups` groups are outstanding.
+  __device__ __forceinline__ static void wait_copies(int groups) {
+    static_assert(RT == 2 || RT == 4 || RT == 8, "groups of a unit");
+    if (RT >= 8 && groups == 4) asm volatile("s_waitcnt vmcnt(%0)" : : "n"(4 * kCopies) : "memory");
+    else if (RT >= 8 && groups == 3) asm volatile("s_waitcnt vmcnt(%0)" : : "n"(3 * kCopies) : "memory");
+    else if (RT >= 4 && groups == 2) asm volatile("s_waitcnt vmcnt(%0)" : : "n"(2 * kCopies) : "memory");
+    else if (groups == 1) asm volatile("s_waitcnt vmcnt(%0)" : : "n"(kCopies) : "memory");
+    else asm volatile("s_waitcnt vmcnt(0)" : : : "memory");
+  }
+
+  // Streams this workgroup's items (blockIdx.x, + gridDim.x, ...).  Wave w takes chunks
+  // c0 + w, c0 + w + W, ... of a unit (c0 < c1).  at(i): the Source of item i; range(i):
+  // its groups, c0 and c1; done(i, scales): called by all waves after its last chunk, in
+  // order, with acc complete and, row-wise, the rows' scales in LDS.  (The products of
+  // sub-tiles that a shorter unit does not read are of whatever the slot holds, and are
+  // not used.)
+  template <class At, class Range, class Done>
+  __device__ __forceinline__ void run(int items, int wave, f32x4 (&acc)[RT][NT], At at,
+                                      Range range, Done done) const {
+    const int stride = (int)gridDim.x;
+    // reading side: the next chunk to issue
+    int ri = (int)blockIdx.x, rn = 0;
+    if (ri >= items) return;
+    Source<RT, NT> rs = at(ri);
+    int rc = rs.c0 + wave;
+    auto more = [&]() __attribute__((always_inline)) {
+      while (ri < items && (rs.groups == 0 || rc >= rs.c1)) {
+        rn += rs.groups > 0;
+        ri += stride;
+        if (ri < items) {
+          rs = at(ri);
+          rc = rs.c0 + wave;
+        }
+      }
+      return ri < items;
+    };
+    auto read = [&](S& side, int slot) __attribute__((always_inline)) {
+      // Wave 0 copies a unit's row scales ahead of its first chunk, so they have
+      // landed when it multiplies that chunk; the other waves see them after the
+      // first barrier of done().  It runs at most two units ahead of done(), whose
+      // barriers every wave has passed for the unit before: four places suffice.
+      if (MODE == kRowwise && wave == 0 && rc == rs.c0)
+#pragma unroll
+        for (int i = 0; i < (RT + 3) / 4; ++i)
+          __builtin_amdgcn_raw_ptr_buffer_load_lds(
+              __builtin_amdgcn_make_buffer_rsrc(const_cast<float*>(rs.row_scale), (short)0,
+                                                0x7fffffff, 0x00020000),
+              (__attribute__((address_space(3))) void*)(row_scale[rn & 3] + 64 * i), 4,
+              rs.row_scale_at[i], 0, 0, 0);
+      issue(rs, rc, side, slot);
+      rc += W;
+    };
+    // multiplying side: item mi, `left` chunks of it to come
+    int mi = (int)blockIdx.x, mn = 0, mg = 0, left = 0;
+    auto begin_unit = [&]() __attribute__((always_inline)) {
+      int c0, c1;
+      range(mi, &mg, &c0, &c1);
+      left = mg > 0 && c1 - c0 > wave ? (c1 - c0 - wave + W - 1) / W : 0;
+#pragma unroll
+      for (int r = 0; r < RT; ++r)
+#pragma unroll
+        for (int n = 0; n < NT; ++n) acc[r][n] = f32x4{0, 0, 0, 0};
+    };
+    S side[2];
+    side[0].groups = side[1].groups = 0;              // 0: nothing issued
+#pragma unroll
+    for (int b = 0; b < 2; ++b)
+      if (more()) read(side[b], b);
+    begin_unit();
+    for (;;) {
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        while (left == 0) {
+          if (mg > 0) done(mi, row_scale[mn++ & 3]);
+          mi += stride;
+          if (mi >= items) return;
+          begin_unit();
+        }
+        // this chunk's copies have landed: at most the next one's are outstanding
+        wait_copies(side[b ^ 1].groups);
+        multiply(side[b], b, acc);
+        --left;
+        side[b].groups = 0;
+        asm volatile("s_waitcnt lgkmcnt(0)" : : : "memory");   // the slot has been read
+        if (more()) read(side[b], b);
+      }
+    }
+  }
 };
 
-template <int RT>
-__device__ __forceinline__ float wave_sum(const float (&v)[kWaves][16][16 * RT + 4], int col,
-                                          int row) {
-  float s = 0.0f;
+// Sums of the W waves, one column tile of a group at a time: [wave][column][row], rows
+// padded by four against bank conflicts.
+template <int W>
+struct Partials {
+  float v[W][16][32 + 4];
+
+  __device__ __forceinline__ float sum(int col, int row) const {
+    float s = 0.0f;
 #pragma unroll
-  for (int w = 0; w < kWaves; ++w) s += v[w][col][row];
-  return s;
+    for (int w = 0; w < W; ++w) s += v[w][col][row];
+    return s;
+  }
+};
+
+// Barrier of the workgroup for data in LDS alone: loads from global memory stay in
+// flight across it.
+__device__ __forceinline__ void lds_barrier() {
+  asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" : : : "memory");
 }
 
-template <int RT, int NT>
-__device__ __forceinline__ void put_partials(Partials<RT>& part, int buf, int wave, int lane,
-                                             const f32x4 (&acc)[RT][NT], int n) {
+// The waves' accumulators of column tile n and sub-tiles 2 j, 2 j + 1 summed through
+// LDS: use(n, j, part) is called when they are there.
+template <int W, int RT, int NT, class Use>
+__device__ __forceinline__ void join_waves(Partials<W>& part, int wave, int lane, int groups,
+                                           const f32x4 (&acc)[RT][NT], Use use) {
 #pragma unroll
-  for (int r = 0; r < RT; ++r)
-    *reinterpret_cast<f32x4*>(&part.v[buf][wave][lane & 15][16 * r + 4 * (lane >> 4)]) = acc[r][n];
+  for (int n = 0; n < NT; ++n)
+#pragma unroll
+    for (int j = 0; j < RT / 2; ++j) {
+      if (j >= groups) break;
+      lds_barrier();                                  // the last readers are done
+#pragma unroll
+      for (int r = 0; r < 2; ++r)
+        *reinterpret_cast<f32x4*>(&part.v[wave][lane & 15][16 * r + 4 * (lane >> 4)]) =
+            acc[2 * j + r][n];
+      lds_barrier();
+      use(n, j);
+    }
 }
 
-// Bytes of a row of `k` codes, and this wave's chunks of it.
+// A float at a wave-uniform address, through the scalar cache.
+__device__ __forceinline__ float uniform_load(const float* p) {
+  return *(const __attribute__((address_space(4))) float*)(uintptr_t)p;
+}
+
+// Bytes of a row of `k` codes.
 template <int FMT>
 __device__ __forceinline__ int row_bytes(int k) {
   return FMT == kE2M1 ? k / 2 : k;
 }
-__device__ __forceinline__ int chunk_at(int chunks, int part, int parts) {
-  return (int)((int64_t)chunks * part / parts);
-}
+
+// All LDS of a kernel in one object, so that the compiler can tell the copies' slots
+// from everything else.
+template <int W, int RT, int CH>
+struct Shared {
+  uint8_t ring[W][2 * RT * 16 * CH];
+  float row_scale[4][RT < 4 ? 64 : 16 * RT];
+  Partials<W> part;
+  Lists l;
+};
 
 struct Workspace {
   int* arrived;                      // [column tiles of the down kernel]
@@ -320,123 +578,111 @@ struct Workspace {
 };
 
 // ---------------------------------------------------------------------------
-// h = act(Wg x) * (Wu x): a tile is 8 * RT gate rows and the same up rows
+// h = act(Wg x) * (Wu x): a group is 16 gate rows (sub-tile 2 j) and their up rows
+// (sub-tile 2 j + 1)
 // ---------------------------------------------------------------------------
-template <int FMT, int MODE, int X, int RT>
-__global__ __launch_bounds__(kThreads, 2) void moe_up_kernel(MoeProblem p, Workspace ws, int tiles,
-                                                             int down_tiles) {
+template <int FMT, int MODE, int X, int W, int RT, int NT, int CH>
+__global__ __launch_bounds__(64 * W, W / 4) void moe_up_kernel(MoeProblem p, Workspace ws,
+                                                               int down_groups) {
   constexpr bool kMx = MODE == kMx32;
-  constexpr int kHalf = 8 * RT;
-  __shared__ Lists l;
-  __shared__ Partials<RT> part;
+  constexpr int kThreads = 64 * W;
+  __shared__ __attribute__((aligned(1024))) Shared<W, RT, CH> lds;
+  Lists& l = lds.l;
   const int t = (int)threadIdx.x, lane = t % 64, grp = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(t / 64);
   // the down kernel's arrival counts start at zero in every call
-  for (int i = (int)blockIdx.x * kThreads + t; i < down_tiles; i += (int)gridDim.x * kThreads)
+  for (int i = (int)blockIdx.x * kThreads + t; i < down_groups; i += (int)gridDim.x * kThreads)
     ws.arrived[i] = 0;
-  build_lists(l, p);
-  const int items = l.used * tiles;
+  build_lists(l, reinterpret_cast<int*>(lds.ring), p, 16 * NT);
   const int bytes = row_bytes<FMT>(p.H);
-  const int chunks = (bytes + kChunk - 1) / kChunk;
-  const int c0 = chunk_at(chunks, wave, kWaves), c1 = chunk_at(chunks, wave + 1, kWaves);
+  const int chunks = (bytes + CH - 1) / CH;
+  const Schedule<RT / 2> plan(l, p.I / 16, 1, 16 * NT);
   constexpr int kXGroup = kFrags<FMT> * 16;          // bytes of a lane group's activations
-  int buf = 0;
-  for (int item = (int)blockIdx.x; item < items; item += (int)gridDim.x) {
-    const int a = item / tiles, row0 = (item - a * tiles) * kHalf;
-    const int e = __builtin_amdgcn_readfirstlane(l.expert[a]);
-    const int first = __builtin_amdgcn_readfirstlane(l.start[a]);
-    const int last = __builtin_amdgcn_readfirstlane(l.start[a + 1]);
-    const uint8_t* w = p.w13 + (int64_t)e * p.stride13;
-    WeightRow row[RT];
+  const float* fs = static_cast<const float*>(p.s13);
+  int ahead = 0, behind = 0, counted = 0;
+  auto range = [&](int u, int* n, int* c0, int* c1) __attribute__((always_inline)) {
+    *n = plan.at(l, u, counted).groups;
+    *c0 = 0;
+    *c1 = chunks;
+  };
+  auto at = [&](int u) __attribute__((always_inline)) {
+    const Unit w = plan.at(l, u, ahead);
+    Source<RT, NT> s;
+    s.groups = w.groups;
+    s.alone = w.alone;
+    s.c0 = 0;
+    s.c1 = chunks;
+    const uint8_t* base = p.w13 + (int64_t)w.e * p.stride13;
+    s.row_scale = fs + (int64_t)w.e * 2 * p.I;
+#pragma unroll
+    for (int i = 0; i < (RT + 3) / 4; ++i) {
+      const int r = 4 * i + (lane >> 4), row = 16 * (w.group + (r >> 1)) + (lane & 15);
+      s.row_scale_at[i] = 4 * ((r & 1) * p.I + (row < p.I ? row : p.I - 1));
+    }
 #pragma unroll
     for (int r = 0; r < RT; ++r) {
-      const int q = 16 * r + (lane & 15);            // row of the tile: gate rows, then up rows
-      const int i = row0 + (q < kHalf ? q : q - kHalf);
-      const int g = (i < p.I ? i : p.I - 1) + (q < kHalf ? 0 : p.I);
-      row[r].codes = w + (int64_t)g * p.ld13 + grp * 16;
-      row[r].scales = kMx ? static_cast<const uint8_t*>(p.s13) +
-                                ((int64_t)e * 2 * p.I + g) * (p.H / 32)
-                          : nullptr;
+      const int i0 = 16 * (w.group + (r >> 1));                // of I; a multiple of 16
+      const int first = (r & 1) * p.I + (i0 < p.I ? i0 : p.I - 16);
+      s.codes[r] = base + (int64_t)first * p.ld13;
+      const int64_t row = (int64_t)w.e * 2 * p.I + first + (lane & 15);
+      s.scales[r] = kMx ? static_cast<const uint8_t*>(p.s13) + row * (p.H / 32) : nullptr;
     }
-    const float* fs = static_cast<const float*>(p.s13);
-    auto columns = [&](int from, auto ntag) __attribute__((always_inline)) {
-      constexpr int NT = decltype(ntag)::value;
-      const uint8_t* col[NT];
 #pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        const int c = from + 16 * n + (lane & 15);
-        col[n] = c < last ? static_cast<const uint8_t*>(p.x) +
-                                (int64_t)(l.list[c] / p.k) * p.ldx * 2 + grp * kXGroup
-                          : nullptr;
-      }
-      f32x4 acc[RT][NT];
-#pragma unroll
-      for (int r = 0; r < RT; ++r)
-#pragma unroll
-        for (int n = 0; n < NT; ++n) acc[r][n] = f32x4{0, 0, 0, 0};
-      stream_rows<FMT, kMx, X, RT, NT>(row, col, bytes, c0, c1, grp, acc);
-#pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        put_partials<RT, NT>(part, buf, wave, lane, acc, n);
-        __syncthreads();
-        for (int o = t; o < 16 * kHalf; o += kThreads) {
-          const int c = o / kHalf, q = o % kHalf, i = row0 + q;
-          const int at = from + 16 * n + c;
-          if (at < last && i < p.I) {
-            float g = wave_sum<RT>(part.v[buf], c, q), u = wave_sum<RT>(part.v[buf], c, q + kHalf);
-            if (MODE == kTensor) {
-              g *= fs[e];
-              u *= fs[e];
-            }
-            if (MODE == kRowwise) {
-              g *= fs[(int64_t)e * 2 * p.I + i];
-              u *= fs[(int64_t)e * 2 * p.I + p.I + i];
-            }
-            __bf16 hi, lo;
-            split_bf16(layer_activate(g, p.act) * u, hi, lo);
-            __bf16* to = reinterpret_cast<__bf16*>(
-                ws.pair + ((int64_t)l.list[at] * p.I + (i & ~7)) * 4) + (i & 7);
-            to[0] = hi;
-            to[8] = lo;
-          }
+    for (int n = 0; n < NT; ++n) {
+      const int c = w.from + 16 * n + (lane & 15);
+      s.col[n] = c < w.last ? l.list[c] / p.k * (int)p.ldx * 2 + grp * kXGroup : kNoColumn;
+    }
+    return s;
+  };
+  f32x4 acc[RT][NT];
+  auto done = [&](int u, const float* scales) __attribute__((always_inline)) {
+    const Unit w = plan.at(l, u, behind);
+    const float ts = MODE == kTensor ? uniform_load(fs + w.e) : 1.0f;
+    join_waves<W, RT, NT>(lds.part, wave, lane, w.groups, acc, [&](int n, int j) {
+      const int c = t / 16, q = t % 16;
+      const int i = 16 * (w.group + j) + q, at = w.from + 16 * n + c;
+      if (c < 16 && at < w.last) {
+        float g = lds.part.sum(c, q), x = lds.part.sum(c, q + 16);
+        if (MODE == kTensor) {
+          g *= ts;
+          x *= ts;
         }
-        buf ^= 1;                     // the other buffer's readers passed the barrier above
+        if (MODE == kRowwise) {
+          g *= scales[32 * j + q];
+          x *= scales[32 * j + 16 + q];
+        }
+        __bf16 hi, lo;
+        split_bf16(layer_activate(g, p.act) * x, hi, lo);
+        __bf16* to = reinterpret_cast<__bf16*>(
+            ws.pair + ((int64_t)l.list[at] * p.I + (i & ~7)) * 4) + (i & 7);
+        to[0] = hi;
+        to[8] = lo;
       }
-    };
-    for (int from = first; from < last;) {
-      const int left = last - from;
-      if (left <= 16) {
-        columns(from, std::integral_constant<int, 1>{});
-        from += 16;
-      } else if (left <= 32) {
-        columns(from, std::integral_constant<int, 2>{});
-        from += 32;
-      } else {
-        columns(from, std::integral_constant<int, 4>{});
-        from += 64;
-      }
-    }
-  }
+    });
+  };
+  const Stream<W, FMT, MODE, X, RT, NT, CH> stream{
+      lds.ring[wave], lds.row_scale,
+      shared_buffer(const_cast<void*>(p.x), (uint32_t)(((p.T - 1) * p.ldx + p.H) * 2)), lane, grp,
+      bytes, p.ld13};
+  stream.run(plan.items, wave, acc, at, range, done);
 }
 
 // ---------------------------------------------------------------------------
-// out = sum over slots of w (W2 h): a tile is 16 * RT rows of W2, K in splits
+// out = sum over slots of w (W2 h): a group is 32 rows of W2; K in parts
 // ---------------------------------------------------------------------------
-template <int FMT, int MODE, typename OutT, int RT>
-__global__ __launch_bounds__(kThreads, 2) void moe_down_kernel(MoeProblem p, Workspace ws,
-                                                               int tiles) {
+template <int FMT, int MODE, typename OutT, int W, int RT, int NT, int CH>
+__global__ __launch_bounds__(64 * W, W / 4) void moe_down_kernel(MoeProblem p, Workspace ws,
+                                                                 int groups) {
   constexpr bool kMx = MODE == kMx32;
-  constexpr int kRows = 16 * RT;
-  __shared__ Lists l;
-  __shared__ Partials<RT> part;
-  __shared__ int s_last;
+  constexpr int kThreads = 64 * W;
+  __shared__ __attribute__((aligned(1024))) Shared<W, RT, CH> lds;
+  Lists& l = lds.l;
   const int t = (int)threadIdx.x, lane = t % 64, grp = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(t / 64);
   const int pairs = p.T * p.k;
-  build_lists(l, p);
-  const int used = l.used;
+  build_lists(l, reinterpret_cast<int*>(lds.ring), p, 16 * NT);
   OutT* out = static_cast<OutT*>(p.out);
-  if (used == 0) {                    // no token has an expert
+  if (l.used == 0) {                  // no token has an expert
     for (int64_t i = (int64_t)blockIdx.x * kThreads + t; i < (int64_t)p.T * (p.H / 4);
          i += (int64_t)gridDim.x * kThreads) {
       const float z[4] = {0, 0, 0, 0};
@@ -444,103 +690,115 @@ __global__ __launch_bounds__(kThreads, 2) void moe_down_kernel(MoeProblem p, Wor
     }
     return;
   }
-  const int items = used * ws.splits * tiles;
   const int bytes = row_bytes<FMT>(p.I);
-  const int chunks = (bytes + kChunk - 1) / kChunk;
+  const int chunks = (bytes + CH - 1) / CH;
+  const Schedule<RT / 2> plan(l, groups, ws.splits, 16 * NT);
   constexpr int kXGroup = kFrags<FMT> * 32;
   const __amdgpu_buffer_rsrc_t rp =
       shared_buffer(ws.partial, (uint32_t)((int64_t)ws.splits * pairs * p.H * 4));
   const float* fs = static_cast<const float*>(p.s2);
-  int buf = 0;
-  for (int item = (int)blockIdx.x; item < items; item += (int)gridDim.x) {
-    const int tile = item % tiles, rest = item / tiles;
-    const int split = rest % ws.splits, a = rest / ws.splits;
-    const int row0 = tile * kRows;
-    const int part0 = split * kWaves + wave, parts = ws.splits * kWaves;
-    const int c0 = chunk_at(chunks, part0, parts), c1 = chunk_at(chunks, part0 + 1, parts);
-    const int e = __builtin_amdgcn_readfirstlane(l.expert[a]);
-    const int first = __builtin_amdgcn_readfirstlane(l.start[a]);
-    const int last = __builtin_amdgcn_readfirstlane(l.start[a + 1]);
-    const uint8_t* w = p.w2 + (int64_t)e * p.stride2;
-    WeightRow row[RT];
+  int ahead = 0, behind = 0, counted = 0;
+  auto chunk_range = [&](int part, int* c0, int* c1) {
+    *c0 = (int)((int64_t)chunks * part / ws.splits);
+    *c1 = (int)((int64_t)chunks * (part + 1) / ws.splits);
+  };
+  auto range = [&](int u, int* n, int* c0, int* c1) __attribute__((always_inline)) {
+    const Unit w = plan.at(l, u, counted);
+    *n = w.groups;
+    chunk_range(w.part, c0, c1);
+  };
+  auto at = [&](int u) __attribute__((always_inline)) {
+    const Unit w = plan.at(l, u, ahead);
+    Source<RT, NT> s;
+    s.groups = w.groups;
+    s.alone = w.alone;
+    chunk_range(w.part, &s.c0, &s.c1);
+    const uint8_t* base = p.w2 + (int64_t)w.e * p.stride2;
+    s.row_scale = fs + (int64_t)w.e * p.H;
+#pragma unroll
+    for (int i = 0; i < (RT + 3) / 4; ++i) {
+      const int row = 32 * w.group + 64 * i + lane;
+      s.row_scale_at[i] = 4 * (row < p.H ? row : p.H - 1);
+    }
 #pragma unroll
     for (int r = 0; r < RT; ++r) {
-      const int q = row0 + 16 * r + (lane & 15);
-      const int g = q < p.H ? q : p.H - 1;
-      row[r].codes = w + (int64_t)g * p.ld2 + grp * 16;
-      row[r].scales = kMx ? static_cast<const uint8_t*>(p.s2) + ((int64_t)e * p.H + g) * (p.I / 32)
-                          : nullptr;
+      const int n0 = 32 * w.group + 16 * r;            // a multiple of 16, as H
+      const int first = n0 < p.H ? n0 : p.H - 16;
+      s.codes[r] = base + (int64_t)first * p.ld2;
+      const int64_t row = (int64_t)w.e * p.H + first + (lane & 15);
+      s.scales[r] = kMx ? static_cast<const uint8_t*>(p.s2) + row * (p.I / 32) : nullptr;
     }
-    auto columns = [&](int from, auto ntag) __attribute__((always_inline)) {
-      constexpr int NT = decltype(ntag)::value;
-      const uint8_t* col[NT];
 #pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        const int c = from + 16 * n + (lane & 15);
-        col[n] = c < last ? ws.pair + (int64_t)l.list[c] * p.I * 4 + grp * kXGroup : nullptr;
-      }
-      f32x4 acc[RT][NT];
+    for (int n = 0; n < NT; ++n) {
+      const int c = w.from + 16 * n + (lane & 15);
+      s.col[n] = c < w.last ? l.list[c] * p.I * 4 + grp * kXGroup : kNoColumn;
+    }
+    return s;
+  };
+  f32x4 acc[RT][NT];
+  auto done = [&](int u, const float* scales) __attribute__((always_inline)) {
+    const Unit w = plan.at(l, u, behind);
+    const float ts = MODE == kTensor ? uniform_load(fs + w.e) : 1.0f;
+    join_waves<W, RT, NT>(lds.part, wave, lane, w.groups, acc, [&](int n, int j) {
 #pragma unroll
-      for (int r = 0; r < RT; ++r)
-#pragma unroll
-        for (int n = 0; n < NT; ++n) acc[r][n] = f32x4{0, 0, 0, 0};
-      stream_rows<FMT, kMx, kXPair, RT, NT>(row, col, bytes, c0, c1, grp, acc);
-#pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        put_partials<RT, NT>(part, buf, wave, lane, acc, n);
-        __syncthreads();
-        for (int o = t; o < 4 * kRows; o += kThreads) {
-          const int c = o / (kRows / 4), q = o % (kRows / 4) * 4;
-          const int at = from + 16 * n + c;
-          if (at < last && row0 + q < p.H) {           // H is a multiple of 16: whole fours
-            f32x4 v;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              v[i] = wave_sum<RT>(part.v[buf], c, q + i);
-              if (MODE == kTensor) v[i] *= fs[e];
-              if (MODE == kRowwise) v[i] *= fs[(int64_t)e * p.H + row0 + q + i];
-            }
-            __builtin_amdgcn_raw_buffer_store_b128(
-                __builtin_bit_cast(u32x4, v), rp,
-                (int)(((split * pairs + l.list[at]) * p.H + row0 + q) * 4), 0, kShared);
-          }
+      for (int o = t; o < 512; o += kThreads) {
+        const int c = o / 32, q = o % 32;              // row q of the group
+        const int at = w.from + 16 * n + c, row = 32 * (w.group + j) + q;
+        if (at < w.last && row < p.H) {
+          float y = lds.part.sum(c, q);
+          if (MODE == kTensor) y *= ts;
+          if (MODE == kRowwise) y *= scales[32 * j + q];
+          __builtin_amdgcn_raw_buffer_store_b32(
+              __float_as_uint(y), rp, (int)(((w.part * pairs + l.list[at]) * p.H + row) * 4), 0,
+              kShared);
         }
-        buf ^= 1;
       }
-    };
-    for (int from = first; from < last;) {
-      const int left = last - from;
-      if (left <= 16) {
-        columns(from, std::integral_constant<int, 1>{});
-        from += 16;
-      } else if (left <= 32) {
-        columns(from, std::integral_constant<int, 2>{});
-        from += 32;
-      } else {
-        columns(from, std::integral_constant<int, 4>{});
-        from += 64;
+    });
+  };
+  const Stream<W, FMT, MODE, kXPair, RT, NT, CH> stream{
+      lds.ring[wave], lds.row_scale, shared_buffer(ws.pair, (uint32_t)((int64_t)pairs * p.I * 4)),
+      lane, grp, bytes, p.ld2};
+  stream.run(plan.items, wave, acc, at, range, done);
+
+  // A group's rows of out are complete when its positions have all arrived.  Arrivals
+  // are counted once per workgroup, after its last unit: a wait for a unit's stores
+  // would also wait for the loads that run ahead of it.  The workgroup that counts a
+  // group's last arrival adds the slots' rows up, in slot order.
+  int* complete = reinterpret_cast<int*>(lds.ring);
+  const int per_group = (int)l.block[l.used] * ws.splits;
+  __builtin_amdgcn_s_waitcnt(0);                       // this thread's rows stored
+  __syncthreads();                                     // ... and every thread's
+  for (int i0 = (int)blockIdx.x; i0 < plan.items; i0 += (int)gridDim.x * (2 * kThreads / RT)) {
+    int group = -1;
+    const int64_t i = i0 + (int64_t)(t / (RT / 2)) * gridDim.x;
+    if (i < plan.items) {
+      int a = 0;
+      const Unit w = plan.template at<false>(l, (int)i, a);
+      if (t % (RT / 2) < w.groups) {
+        group = w.group + t % (RT / 2);
+        if (__hip_atomic_fetch_add(&ws.arrived[group], 1, __ATOMIC_RELAXED,
+                                   __HIP_MEMORY_SCOPE_AGENT) != per_group - 1)
+          group = -1;
       }
     }
-    // the last of a tile's workgroups adds the slots' rows up
-    __builtin_amdgcn_s_waitcnt(0);                     // this thread's rows stored
-    __syncthreads();                                   // ... and every thread's
-    if (t == 0)
-      s_last = __hip_atomic_fetch_add(&ws.arrived[tile], 1, __ATOMIC_RELAXED,
-                                      __HIP_MEMORY_SCOPE_AGENT) == used * ws.splits - 1;
+    complete[t] = group;
     __syncthreads();
-    if (s_last) {
-      for (int o = t; o < p.T * (kRows / 4); o += kThreads) {
-        const int tok = o / (kRows / 4), q = row0 + o % (kRows / 4) * 4;
+    for (int c = 0; c < kThreads; ++c) {
+      if (i0 + (int64_t)(c / (RT / 2)) * gridDim.x >= plan.items) break;
+      const int row0 = complete[c] * 32;
+      if (row0 < 0) continue;
+      for (int o = t; o < p.T * 8; o += kThreads) {
+        const int tok = o / 8, q = row0 + o % 8 * 4;
         if (q >= p.H) continue;
         float y[4] = {0, 0, 0, 0};
         for (int j = 0; j < p.k; ++j) {
-          const int i = tok * p.k + j;
-          if ((unsigned)p.ids[i] >= (unsigned)p.E) continue;
-          const float wt = p.weights[i];
+          const int at = tok * p.k + j;
+          if ((unsigned)p.ids[at] >= (unsigned)p.E) continue;
+          const float wt = p.weights[at];
           for (int s = 0; s < ws.splits; ++s) {
             const f32x4 v = __builtin_bit_cast(
                 f32x4, __builtin_amdgcn_raw_buffer_load_b128(
-                           rp, (int)(((s * pairs + i) * p.H + q) * 4), 0, kShared));
+                           rp, (int)(((s * pairs + at) * p.H + q) * 4), 0, kShared));
 #pragma unroll
             for (int c = 0; c < 4; ++c) y[c] += wt * v[c];
           }
@@ -548,25 +806,29 @@ __global__ __launch_bounds__(kThreads, 2) void moe_down_kernel(MoeProblem p, Wor
         store4(out + (int64_t)tok * p.ldo + q, y);
       }
     }
-    __syncthreads();                                   // s_last is read before it is set again
+    __syncthreads();
   }
 }
 
 // ---------------------------------------------------------------------------
 // Launch
 // ---------------------------------------------------------------------------
-constexpr int kRt = 2;                 // tiles of 16 rows per workgroup step
+// Eight waves, units of 64 rows in chunks of 128 bytes: two slots of all waves fill 128
+// KiB of LDS, which is what the copies need in flight (units of 32 rows, or of 64 in
+// chunks of 256 bytes by four waves, 3-6 % slower; four waves of 128 rows 20 %).
+constexpr int kW = 8, kRt = 4, kCh = 128;
 
-constexpr size_t round16(size_t v) { return (v + 255) / 256 * 256; }
+constexpr size_t round256(size_t v) { return (v + 255) / 256 * 256; }
 
-int down_tiles(int64_t H) { return (int)((H + 16 * kRt - 1) / (16 * kRt)); }
+int down_groups(int64_t H) { return (int)((H + 31) / 32); }
 
-// K splits of the down kernel: enough work items for two workgroups per CU.
+// Parts of the down kernel's K: a unit for every CU at least, where K is long enough to be
+// worth the partial rows.
 int down_splits(int64_t T, int64_t H, int64_t I, int E, int k) {
   const int64_t pairs = T * k;
-  const int64_t items = down_tiles(H) * (pairs < E ? pairs : E);
+  const int64_t units = (down_groups(H) + 1) / 2 * (pairs < E ? pairs : E);
   int s = 1;
-  while (s < 8 && items * s < 512 && I / (2 * s) >= 1024) s *= 2;
+  while (s < 8 && units * s < 256 && I / (2 * s) >= 1024) s *= 2;
   return s;
 }
 
@@ -575,9 +837,9 @@ Workspace moe_layout(void* base, int64_t T, int64_t H, int64_t I, int E, int k, 
   uint8_t* b = static_cast<uint8_t*>(base);
   size_t at = kSplitCounterBytes;      // the GEMMs' split-K counters: left alone
   ws.arrived = reinterpret_cast<int*>(b + at);
-  at += round16((size_t)down_tiles(H) * 4);
+  at += round256((size_t)down_groups(H) * 4);
   ws.pair = b + at;
-  at += round16((size_t)T * k * I * 4);
+  at += round256((size_t)T * k * I * 4);
   ws.partial = reinterpret_cast<float*>(b + at);
   ws.splits = down_splits(T, H, I, E, k);
   at += (size_t)ws.splits * T * k * H * 4;
@@ -585,21 +847,28 @@ Workspace moe_layout(void* base, int64_t T, int64_t H, int64_t I, int E, int k, 
   return ws;
 }
 
-template <int FMT, int MODE, int X, typename OutT>
-hipError_t launch_as(const MoeProblem& p, hipStream_t stream) {
+template <int FMT, int MODE, int X, typename OutT, int NT>
+hipError_t launch_columns(const MoeProblem& p, hipStream_t stream) {
   size_t total;
   const Workspace ws = moe_layout(p.workspace, p.T, p.H, p.I, p.E, p.k, &total);
-  const int64_t pairs = (int64_t)p.T * p.k, most = pairs < p.E ? pairs : p.E;
-  const int64_t slots = 2 * (int64_t)device_cu_count();
-  const int up = (p.I + 8 * kRt - 1) / (8 * kRt), down = down_tiles(p.H);
-  const int64_t up_items = most * up, down_items = most * down * ws.splits;
-  hipLaunchKernelGGL((moe_up_kernel<FMT, MODE, X, kRt>),
-                     dim3((unsigned)(up_items < slots ? up_items : slots)), dim3(kThreads), 0,
-                     stream, p, ws, up, down);
-  hipLaunchKernelGGL((moe_down_kernel<FMT, MODE, OutT, kRt>),
-                     dim3((unsigned)(down_items < slots ? down_items : slots)), dim3(kThreads), 0,
-                     stream, p, ws, down);
+  const unsigned cus = (unsigned)device_cu_count();
+  const int groups = down_groups(p.H);
+  hipLaunchKernelGGL((moe_up_kernel<FMT, MODE, X, kW, kRt, NT, kCh>), dim3(cus), dim3(64 * kW), 0,
+                     stream, p, ws, groups);
+  hipLaunchKernelGGL((moe_down_kernel<FMT, MODE, OutT, kW, kRt, NT, kCh>), dim3(cus),
+                     dim3(64 * kW), 0, stream, p, ws, groups);
   return hipGetLastError();
+}
+
+template <int FMT, int MODE, int X, typename OutT>
+hipError_t launch_as(const MoeProblem& p, hipStream_t stream) {
+  // Column blocks of 32 where an expert has more than 16 pairs on average: E4M3, 8 experts
+  // of 4096 x 14336, two per token: 371 against 372 us at 64 tokens, 527 against 597 at
+  // 128 (292 against 278 at 32).  E2M1 fragments take the registers that these need.
+  if constexpr (FMT != kE2M1)
+    if ((int64_t)p.T * p.k > 16 * (int64_t)p.E)
+      return launch_columns<FMT, MODE, X, OutT, 2>(p, stream);
+  return launch_columns<FMT, MODE, X, OutT, 1>(p, stream);
 }
 
 template <int FMT, int MODE>
