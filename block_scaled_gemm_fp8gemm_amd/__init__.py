@@ -361,14 +361,21 @@ def fp8gemm_version() -> int:
 
 
 # ---- PyTorch conveniences ---------------------------------------------------
+_torch_module = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
 
 
 def _stream_handle(device) -> int:
     torch = _torch()
-    return torch.cuda.current_stream(device).cuda_stream
+    # an index costs half of what a device object does here
+    return torch.cuda.current_stream(device.index).cuda_stream
 
 
 def _require_cuda(t, name, dtype=None, dim=None):
@@ -399,7 +406,13 @@ def gemm_workspace(device, nbytes: int):
     """
     torch = _torch()
     dev = torch.device(device)
-    key = (dev, torch.cuda.current_stream(dev).cuda_stream)
+    return _stream_workspace(dev, _stream_handle(dev), nbytes)
+
+
+def _stream_workspace(dev, stream, nbytes):
+    """gemm_workspace for a device and its current stream's handle."""
+    torch = _torch()
+    key = (dev, stream)
     ws = _WORKSPACES.get(key)
     if ws is None or ws.numel() < nbytes:
         ws = torch.zeros(nbytes, dtype=torch.uint8, device=dev)
@@ -614,11 +627,17 @@ def grouped_gemm(qa, sa, offsets, qb, sb, mode: str = "rowwise", out_dtype: str 
 
 
 # ---- serving operators ----------------------------------------------------------
-@functools.lru_cache(maxsize=None)
+# These calls take microseconds on the GPU, so their checks are kept few and cheap:
+# one comparison of type, shape and device per tensor, and the message only on failure.
+_DTYPE_CODES = {}
+
+
 def _dtype_code(dtype):
     """fp8gemm dtype of a torch activation type (None: not one)."""
-    torch = _torch()
-    return {torch.float16: 0, torch.bfloat16: 1, torch.float32: 2}.get(dtype)
+    if not _DTYPE_CODES:
+        torch = _torch()
+        _DTYPE_CODES.update({torch.float16: 0, torch.bfloat16: 1, torch.float32: 2})
+    return _DTYPE_CODES.get(dtype)
 
 
 def _require(cond, message):
@@ -626,17 +645,31 @@ def _require(cond, message):
         raise ValueError(message)
 
 
-def _require_like(t, name, device, dtype, shape):
-    """`t` is a CUDA tensor of this device, type and shape, unit stride in its last
-    dimension (a size of None is not checked)."""
+def _like(t, name, device, dtype, shape):
+    """Checks that `t` is a CUDA tensor of this device, type and shape with unit stride in
+    its last dimension."""
+    if t.dtype == dtype and t.shape == shape and t.device == device and \
+            (t.stride(-1) == 1 or t.shape[-1] <= 1):
+        return
     if not t.is_cuda or t.device != device:
         raise ValueError(f"{name} must be a CUDA (HIP) tensor on {device}")
     if t.dtype != dtype:
         raise ValueError(f"{name} must have dtype {dtype}, got {t.dtype}")
-    if t.dim() != len(shape) or any(n is not None and n != m for n, m in zip(shape, t.shape)):
+    if t.shape != shape:
         raise ValueError(f"{name} must have shape {list(shape)}, got {list(t.shape)}")
-    if t.dim() and t.shape[-1] > 1 and t.stride(-1) != 1:
-        raise ValueError(f"{name} must have unit stride in its last dimension")
+    raise ValueError(f"{name} must have unit stride in its last dimension")
+
+
+def _activations(x):
+    """Checks the activations x [T, K]; returns their device and dtype code."""
+    if not x.is_cuda or x.dim() != 2:
+        raise ValueError("x must be a 2-D CUDA (HIP) tensor")
+    code = _dtype_code(x.dtype)
+    if code != 0 and code != 1:
+        raise ValueError(f"x must be float16 or bfloat16, got {x.dtype}")
+    if x.stride(1) != 1 and x.shape[1] > 1:
+        raise ValueError("x must have unit stride in its last dimension")
+    return x.device, code
 
 
 def _row_pitch(t):
@@ -653,27 +686,30 @@ def _padded(rows, cols, dtype, device):
     return out if pitch == cols else out[:, :cols]
 
 
-def _routing_outputs(T, k, device, ids, weights):
+def _routing(T, k, device, ids, weights):
+    """ids int32 and weights float32 [T, k], checked or new."""
     torch = _torch()
     if ids is None:
         ids = torch.empty((T, k), dtype=torch.int32, device=device)
     else:
-        _require_like(ids, "ids", device, torch.int32, (T, k))
+        _like(ids, "ids", device, torch.int32, (T, k))
         _require(ids.is_contiguous(), "ids must be contiguous")
     if weights is None:
         weights = torch.empty((T, k), dtype=torch.float32, device=device)
     else:
-        _require_like(weights, "weights", device, torch.float32, (T, k))
+        _like(weights, "weights", device, torch.float32, (T, k))
         _require(weights.is_contiguous(), "weights must be contiguous")
     return ids, weights
 
 
 def _check_logits(logits):
-    _require(logits.is_cuda and logits.dim() == 2, "logits must be a 2-D CUDA (HIP) tensor")
+    if not logits.is_cuda or logits.dim() != 2:
+        raise ValueError("logits must be a 2-D CUDA (HIP) tensor")
     code = _dtype_code(logits.dtype)
-    _require(code is not None, f"logits must be float32, float16 or bfloat16, got {logits.dtype}")
-    _require(logits.shape[1] <= 1 or logits.stride(1) == 1,
-             "logits must have unit stride in its last dimension")
+    if code is None:
+        raise ValueError(f"logits must be float32, float16 or bfloat16, got {logits.dtype}")
+    if logits.stride(1) != 1 and logits.shape[1] > 1:
+        raise ValueError("logits must have unit stride in its last dimension")
     return code
 
 
@@ -686,10 +722,10 @@ def moe_route(logits, k: int, scoring: str = "softmax", renormalize: bool = True
     weight 0."""
     code = _check_logits(logits)
     T, E = logits.shape
-    ids, weights = _routing_outputs(T, k, logits.device, ids, weights)
+    device = logits.device
+    ids, weights = _routing(T, k, device, ids, weights)
     fp8gemm_moe_route(_ptr(logits), code, T, _row_pitch(logits), E, k, SCORINGS[scoring],
-                      int(renormalize), scale, _ptr(ids), _ptr(weights),
-                      _stream_handle(logits.device))
+                      int(renormalize), scale, _ptr(ids), _ptr(weights), _stream_handle(device))
     return ids, weights
 
 
@@ -701,63 +737,61 @@ def group_rows(ids, groups: int, order=None, offsets=None, workspace=None):
     With moe_route's ids, order // k are the tokens sorted by expert and offsets the
     offsets of ``grouped_gemm``; with the rows' adapter ids, the plan of ``lora``."""
     torch = _torch()
-    _require(ids.is_cuda and ids.dtype == torch.int32 and ids.is_contiguous(),
-             "ids must be a contiguous int32 CUDA (HIP) tensor")
-    n = ids.numel()
+    if not ids.is_cuda or ids.dtype != torch.int32 or not ids.is_contiguous():
+        raise ValueError("ids must be a contiguous int32 CUDA (HIP) tensor")
+    n, device = ids.numel(), ids.device
     if order is None:
-        order = torch.empty(n, dtype=torch.int32, device=ids.device)
+        order = torch.empty(n, dtype=torch.int32, device=device)
     else:
-        _require_like(order, "order", ids.device, torch.int32, (n,))
+        _like(order, "order", device, torch.int32, (n,))
     if offsets is None:
-        offsets = torch.empty(groups + 1, dtype=torch.int32, device=ids.device)
+        offsets = torch.empty(max(groups, 0) + 1, dtype=torch.int32, device=device)
     else:
-        _require_like(offsets, "offsets", ids.device, torch.int32, (groups + 1,))
+        _like(offsets, "offsets", device, torch.int32, (groups + 1,))
     need = fp8gemm_group_rows_workspace_size(n, groups)
     if need and workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=ids.device)
+        workspace = torch.empty(need, dtype=torch.uint8, device=device)
     fp8gemm_group_rows(_ptr(ids), n, groups, _ptr(order), _ptr(offsets),
                        _ptr(workspace) if need else 0, workspace.numel() if need else 0,
-                       _stream_handle(ids.device))
+                       _stream_handle(device))
     return order, offsets
 
 
 @functools.lru_cache(maxsize=256)
 def _moe_workspace_need(T, H, I, E, k):
-    return fp8gemm_moe_workspace_size(T, H, I, E, k)
+    return max(fp8gemm_moe_workspace_size(T, H, I, E, k), 1)
 
 
 def _check_experts(x, qw13, sw13, qw2, sw2, mode, fmt):
-    """Shapes of a layer's tensors: (T, H, I, E)."""
+    """Shapes of a layer's tensors: (T, H, I, E, device, dtype code)."""
     torch = _torch()
-    _require(x.is_cuda and x.dim() == 2, "x must be a 2-D CUDA (HIP) tensor")
-    _require(x.dtype in (torch.float16, torch.bfloat16),
-             f"x must be float16 or bfloat16, got {x.dtype}")
-    _require(x.shape[1] <= 1 or x.stride(1) == 1, "x must have unit stride in its last dimension")
+    device, code = _activations(x)
     T, H = x.shape
-    _require(qw2.dim() == 3, "qw2 must be 3-D")
+    if qw2.dim() != 3:
+        raise ValueError("qw2 must be 3-D")
     bits = CODE_BITS[fmt]
-    E, I = qw2.shape[0], qw2.shape[2] * 8 // bits
-    _require_like(qw13, "qw13", x.device, torch.uint8, (E, 2 * I, H * bits // 8))
-    _require_like(qw2, "qw2", x.device, torch.uint8, (E, H, None))
+    E, _, inner = qw2.shape
+    I = inner * 8 // bits
+    _like(qw13, "qw13", device, torch.uint8, (E, 2 * I, H * bits // 8))
+    _like(qw2, "qw2", device, torch.uint8, (E, H, inner))
     for name, s, n, c in (("sw13", sw13, 2 * I, H), ("sw2", sw2, H, I)):
         if mode == "mx32":
-            _require_like(s, name, x.device, torch.uint8, (E, n, c // 32))
-        else:
-            _require(s.is_cuda and s.device == x.device and s.dtype == torch.float32 and
-                     s.numel() == (E if mode == "tensor" else E * n),
-                     f"{name} must be a float32 CUDA (HIP) tensor of "
-                     f"{E if mode == 'tensor' else E * n} scales")
+            _like(s, name, device, torch.uint8, (E, n, c // 32))
+        elif s.dtype != torch.float32 or s.numel() != (E if mode == "tensor" else E * n) or \
+                s.device != device:
+            raise ValueError(f"{name} must be a float32 CUDA (HIP) tensor of "
+                             f"{E if mode == 'tensor' else E * n} scales")
         _require(s.is_contiguous(), f"{name} must be contiguous")
-    return T, H, I, E
+    return T, H, I, E, device, code
 
 
-def _layer_buffers(x, T, H, I, E, k, out, workspace):
+def _layer_buffers(x, T, H, I, E, k, device, stream, out, workspace):
     if out is None:
-        out = _padded(T, H, x.dtype, x.device)
+        out = _padded(T, H, x.dtype, device)
     else:
-        _require_like(out, "out", x.device, x.dtype, (T, H))
+        _like(out, "out", device, x.dtype, (T, H))
     if workspace is None:
-        workspace = gemm_workspace(x.device, max(_moe_workspace_need(T, H, I, E, k), 1))
+        workspace = _stream_workspace(device, stream, _moe_workspace_need(T, H, I, E, k))
     return out, workspace
 
 
@@ -771,17 +805,18 @@ def moe_experts(x, ids, weights, qw13, sw13, qw2, sw2, mode: str = "rowwise",
     qw2 uint8 [E, H, I]: e4m3 codes, or e2m1 with mode "mx32" (two codes per byte);
     sw13, sw2 as ``grouped_gemm``'s sb: float32 [E] (tensor), [E * rows] (rowwise), uint8
     [E, rows, K / 32] (mx32).  One set of weights serves this call and ``grouped_gemm``."""
-    torch = _torch()
-    T, H, I, E = _check_experts(x, qw13, sw13, qw2, sw2, mode, fmt)
-    _require(ids.dim() == 2, "ids must be 2-D")
+    T, H, I, E, device, code = _check_experts(x, qw13, sw13, qw2, sw2, mode, fmt)
+    if ids.dim() != 2:
+        raise ValueError("ids must be 2-D")
     k = ids.shape[1]
-    ids, weights = _routing_outputs(T, k, x.device, ids, weights)
-    out, workspace = _layer_buffers(x, T, H, I, E, k, out, workspace)
-    fp8gemm_moe_run(T, H, I, E, k, _ptr(x), _row_pitch(x), _dtype_code(x.dtype), _ptr(ids),
-                    _ptr(weights), _ptr(qw13), qw13.stride(1), qw13.stride(0), _ptr(sw13),
-                    _ptr(qw2), qw2.stride(1), qw2.stride(0), _ptr(sw2), SCALE_MODES[mode],
-                    FORMATS[fmt], ACTIVATIONS[activation], _ptr(out), _row_pitch(out),
-                    _ptr(workspace), workspace.numel(), _stream_handle(x.device))
+    ids, weights = _routing(T, k, device, ids, weights)
+    stream = _stream_handle(device)
+    out, workspace = _layer_buffers(x, T, H, I, E, k, device, stream, out, workspace)
+    fp8gemm_moe_run(T, H, I, E, k, _ptr(x), _row_pitch(x), code, _ptr(ids), _ptr(weights),
+                    _ptr(qw13), qw13.stride(1), qw13.stride(0), _ptr(sw13), _ptr(qw2),
+                    qw2.stride(1), qw2.stride(0), _ptr(sw2), SCALE_MODES[mode], FORMATS[fmt],
+                    ACTIVATIONS[activation], _ptr(out), _row_pitch(out), _ptr(workspace),
+                    workspace.numel(), stream)
     return out
 
 
@@ -791,25 +826,25 @@ def moe_layer(x, logits, qw13, sw13, qw2, sw2, k: int, mode: str = "rowwise",
               workspace=None):
     """(out [T, H], ids, weights): a whole mixture-of-experts layer for at most 128 tokens,
     ``moe_route`` on the router's logits [T, E] and ``moe_experts`` on its choice."""
-    T, H, I, E = _check_experts(x, qw13, sw13, qw2, sw2, mode, fmt)
-    code = _check_logits(logits)
-    _require(logits.device == x.device and tuple(logits.shape) == (T, E),
-             f"logits must have shape {[T, E]} on {x.device}")
-    ids, weights = _routing_outputs(T, k, x.device, ids, weights)
-    out, workspace = _layer_buffers(x, T, H, I, E, k, out, workspace)
-    fp8gemm_moe_layer(T, H, I, E, k, _ptr(x), _row_pitch(x), _dtype_code(x.dtype), _ptr(logits),
-                      _row_pitch(logits), code, SCORINGS[scoring], int(renormalize), scale,
+    T, H, I, E, device, code = _check_experts(x, qw13, sw13, qw2, sw2, mode, fmt)
+    logits_code = _check_logits(logits)
+    if logits.shape != (T, E) or logits.device != device:
+        raise ValueError(f"logits must have shape {[T, E]} on {device}")
+    ids, weights = _routing(T, k, device, ids, weights)
+    stream = _stream_handle(device)
+    out, workspace = _layer_buffers(x, T, H, I, E, k, device, stream, out, workspace)
+    fp8gemm_moe_layer(T, H, I, E, k, _ptr(x), _row_pitch(x), code, _ptr(logits),
+                      _row_pitch(logits), logits_code, SCORINGS[scoring], int(renormalize), scale,
                       _ptr(ids), _ptr(weights), _ptr(qw13), qw13.stride(1), qw13.stride(0),
                       _ptr(sw13), _ptr(qw2), qw2.stride(1), qw2.stride(0), _ptr(sw2),
                       SCALE_MODES[mode], FORMATS[fmt], ACTIVATIONS[activation], _ptr(out),
-                      _row_pitch(out), _ptr(workspace), workspace.numel(),
-                      _stream_handle(x.device))
+                      _row_pitch(out), _ptr(workspace), workspace.numel(), stream)
     return out, ids, weights
 
 
 @functools.lru_cache(maxsize=256)
 def _lora_workspace_need(M, K, rank, groups):
-    return fp8gemm_lora_workspace_size(M, K, rank, groups)
+    return max(fp8gemm_lora_workspace_size(M, K, rank, groups), 1)
 
 
 def lora(x, base, lora_a, lora_b, order, offsets, scales=None, activation: str = "none",
@@ -823,31 +858,30 @@ def lora(x, base, lora_a, lora_b, order, offsets, scales=None, activation: str =
     ``group_rows(adapter_ids, G)``; one plan serves every projection of a step.  scales:
     float32 [G] or None.  out may be base."""
     torch = _torch()
-    _require(x.is_cuda and x.dim() == 2, "x must be a 2-D CUDA (HIP) tensor")
-    _require(x.dtype in (torch.float16, torch.bfloat16),
-             f"x must be float16 or bfloat16, got {x.dtype}")
-    _require(x.shape[1] <= 1 or x.stride(1) == 1, "x must have unit stride in its last dimension")
-    _require(lora_a.dim() == 3 and base.dim() == 2, "lora_a must be 3-D and base 2-D")
+    device, code = _activations(x)
+    if lora_a.dim() != 3 or base.dim() != 2:
+        raise ValueError("lora_a must be 3-D and base 2-D")
     M, K = x.shape
-    G, rank = lora_a.shape[:2]
+    G, rank, _ = lora_a.shape
     N = base.shape[1]
-    dev, dt = x.device, x.dtype
-    _require_like(base, "base", dev, dt, (M, N))
-    _require_like(lora_a, "lora_a", dev, dt, (G, rank, K))
-    _require_like(lora_b, "lora_b", dev, dt, (G, N, rank))
-    _require_like(order, "order", dev, torch.int32, (M,))
-    _require_like(offsets, "offsets", dev, torch.int32, (G + 1,))
+    dt = x.dtype
+    _like(base, "base", device, dt, (M, N))
+    _like(lora_a, "lora_a", device, dt, (G, rank, K))
+    _like(lora_b, "lora_b", device, dt, (G, N, rank))
+    _like(order, "order", device, torch.int32, (M,))
+    _like(offsets, "offsets", device, torch.int32, (G + 1,))
     if scales is not None:
-        _require_like(scales, "scales", dev, torch.float32, (G,))
+        _like(scales, "scales", device, torch.float32, (G,))
     if out is None:
-        out = _padded(M, N, dt, dev)
+        out = _padded(M, N, dt, device)
     elif out is not base:
-        _require_like(out, "out", dev, dt, (M, N))
+        _like(out, "out", device, dt, (M, N))
+    stream = _stream_handle(device)
     if workspace is None:
-        workspace = gemm_workspace(dev, max(_lora_workspace_need(M, K, rank, G), 1))
-    fp8gemm_lora_run(M, N, K, rank, G, _ptr(x), _row_pitch(x), _ptr(base), _row_pitch(base),
-                     _dtype_code(dt), _ptr(lora_a), lora_a.stride(1), lora_a.stride(0),
-                     _ptr(lora_b), lora_b.stride(1), lora_b.stride(0), _ptr(order), _ptr(offsets),
-                     _ptr(scales), ACTIVATIONS[activation], _ptr(out), _row_pitch(out),
-                     _ptr(workspace), workspace.numel(), _stream_handle(dev))
+        workspace = _stream_workspace(device, stream, _lora_workspace_need(M, K, rank, G))
+    fp8gemm_lora_run(M, N, K, rank, G, _ptr(x), _row_pitch(x), _ptr(base), _row_pitch(base), code,
+                     _ptr(lora_a), lora_a.stride(1), lora_a.stride(0), _ptr(lora_b),
+                     lora_b.stride(1), lora_b.stride(0), _ptr(order), _ptr(offsets), _ptr(scales),
+                     ACTIVATIONS[activation], _ptr(out), _row_pitch(out), _ptr(workspace),
+                     workspace.numel(), stream)
     return out

@@ -49,6 +49,7 @@ struct Lists {
   uint16_t start[kMaxExperts + 2];   // their pairs: list[start[a] .. start[a+1])
   uint16_t block[kMaxExperts + 2];   // their column blocks, counted through
   uint16_t list[kMaxPairs];          // pair = token * k + slot
+  uint8_t token[kMaxPairs];
   int used;
 };
 
@@ -114,7 +115,10 @@ __device__ __forceinline__ void build_lists(Lists& l, int* count, const MoeProbl
       __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
       if (live && (same >> t) == 1ull) count[e] = at + 1;
       __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-      if (live) l.list[at] = (uint16_t)i;
+      if (live) {
+        l.list[at] = (uint16_t)i;
+        l.token[at] = (uint8_t)(i / p.k);
+      }
     }
   }
   __syncthreads();
@@ -160,11 +164,16 @@ struct Schedule {
     piece = __builtin_amdgcn_readfirstlane(piece);
   }
 
-  // Item i (UNIFORM: the same in every lane).  a: a place in the list of active experts not
-  // past its expert's, moved there.
-  template <bool UNIFORM = true>
-  __device__ __forceinline__ Unit at(const Lists& l, int i, int& a) const {
-    auto value = [](int v) { return UNIFORM ? __builtin_amdgcn_readfirstlane(v) : v; };
+  // Items of this workgroup: blockIdx.x, + gridDim.x, ...
+  __device__ __forceinline__ int count() const {
+    return items > (int)blockIdx.x
+               ? (items - (int)blockIdx.x + (int)gridDim.x - 1) / (int)gridDim.x : 0;
+  }
+
+  // Item i.  (Half a dozen divisions: the workgroup looks its items up ahead of time, see
+  // Units.)
+  __device__ __forceinline__ Unit at(const Lists& l, int i) const {
+    int a = 0;
     int unit = i, first = 0, most = NP;
     if (i >= whole) {
       const int per = NP / piece, q = i - whole;
@@ -172,9 +181,18 @@ struct Schedule {
       first = q % per * piece;
       most = piece;
     }
-    while (unit >= value(l.block[a + 1]) * parts * tiles) ++a;
-    const int b0 = value(l.block[a]);
-    const int blocks = value(l.block[a + 1]) - b0;
+    // its expert: the last with block[a] * parts * tiles <= unit
+    for (int lo = 0, hi = l.used - 1; lo <= hi;) {
+      const int mid = (lo + hi) >> 1;
+      if (l.block[mid] * parts * tiles <= unit) {
+        a = mid;
+        lo = mid + 1;
+      } else {
+        hi = mid - 1;
+      }
+    }
+    const int b0 = l.block[a];
+    const int blocks = l.block[a + 1] - b0;
     const int local = unit - b0 * parts * tiles;       // part by part, eight tiles by eight
     Unit w;
     w.part = local / (blocks * tiles);
@@ -183,15 +201,53 @@ struct Schedule {
     const int run = tiles - first8 < 8 ? tiles - first8 : 8;
     const int in_run = in_part - first8 * blocks;
     const int block = in_run / run;
-    w.e = value(l.expert[a]);
+    w.e = l.expert[a];
     w.group = (first8 + in_run - block * run) * NP + first;
     w.groups = groups - w.group < most ? groups - w.group : most;
     w.groups = w.groups < 0 ? 0 : w.groups;
-    w.from = value(l.start[a]) + block * cols;
-    const int last = value(l.start[a + 1]);
+    w.from = l.start[a] + block * cols;
+    const int last = l.start[a + 1];
     w.last = w.from + cols < last ? w.from + cols : last;
     w.alone = blocks == 1;
     return w;
+  }
+};
+
+// The workgroup's items in LDS, eight places: item n of the workgroup (the n-th it takes)
+// is looked up while item n - kAhead is finished, by one wave in turn.
+constexpr int kAhead = 4;
+struct Units {
+  Unit u[8];
+
+  __device__ __forceinline__ Unit get(int n) const {
+    const Unit& v = u[n & 7];
+    Unit w;
+    w.e = __builtin_amdgcn_readfirstlane(v.e);
+    w.part = __builtin_amdgcn_readfirstlane(v.part);
+    w.group = __builtin_amdgcn_readfirstlane(v.group);
+    w.groups = __builtin_amdgcn_readfirstlane(v.groups);
+    w.from = __builtin_amdgcn_readfirstlane(v.from);
+    w.last = __builtin_amdgcn_readfirstlane(v.last);
+    w.alone = __builtin_amdgcn_readfirstlane(v.alone);
+    return w;
+  }
+  template <int NP>
+  __device__ __forceinline__ void look_up(const Schedule<NP>& plan, const Lists& l, int n) {
+    const int64_t i = blockIdx.x + (int64_t)n * gridDim.x;
+    if (i < plan.items) u[n & 7] = plan.at(l, (int)i);
+  }
+  // The first items (all threads; ends with a barrier).
+  template <int NP>
+  __device__ __forceinline__ void look_up_first(const Schedule<NP>& plan, const Lists& l) {
+    if ((int)threadIdx.x < kAhead) look_up(plan, l, (int)threadIdx.x);
+    __syncthreads();
+  }
+  // While item n is finished (all waves, before its barriers): item n + kAhead, which no
+  // wave reads before the barriers of item n + 1.
+  template <int NP>
+  __device__ __forceinline__ void look_up_next(const Schedule<NP>& plan, const Lists& l, int n,
+                                               int wave, int waves) {
+    if (n % waves == wave && threadIdx.x % 64 == 0) look_up(plan, l, n + kAhead);
   }
 };
 
@@ -258,6 +314,7 @@ struct Side {
   static constexpr int kF = kFrags<FMT>;
   static constexpr int kXFrag = X == kXPair ? 32 : 16;      // bytes of 8 activations
   static constexpr int kCodes = FMT == kE2M1 ? CH / 16 : CH / 32;   // MX scale codes of a row
+  static_assert(kCodes == 4 || kCodes == 8, "one or two words");
   uint32_t sc[MX ? RT : 1][(kCodes + 3) / 4];
   u32x4 x[kSteps][NT][kF][kXFrag / 16];
   int c;                                                    // which chunk
@@ -291,7 +348,7 @@ struct Stream {
   uint8_t* ring;                                      // this wave's two slots
   float (*row_scale)[RT < 4 ? 64 : 16 * RT];          // row-wise: the rows' scales, by unit
   __amdgpu_buffer_rsrc_t x;                           // the activations
-  int lane, grp, bytes;                               // bytes: of a weight row
+  int lane, grp, bytes, parts;                        // bytes: of a weight row; parts of K
   int64_t ld;
 
   // Starts the loads of chunk c: the side registers, then the codes to slot `slot`.
@@ -322,17 +379,15 @@ struct Stream {
       for (int r = 0; r < RT; ++r) {
         if (full) {
           __builtin_memcpy(side.sc[r], src.scales[r] + c * S::kCodes, S::kCodes);
+        } else if (blocks >= S::kCodes) {             // the row's last codes, moved down
+          uint64_t v = 0;
+          __builtin_memcpy(&v, src.scales[r] + blocks - S::kCodes, S::kCodes);
+          v >>= 8 * ((c + 1) * S::kCodes - blocks);
+          __builtin_memcpy(side.sc[r], &v, (S::kCodes + 3) / 4 * 4);
         } else {
-#pragma unroll
-          for (int i = 0; i < (S::kCodes + 3) / 4; ++i) {
-            side.sc[r][i] = 0;
-#pragma unroll
-            for (int b = 0; b < 4; ++b) {
-              const int at = c * S::kCodes + 4 * i + b;
-              if (4 * i + b < S::kCodes && at < blocks)
-                side.sc[r][i] |= (uint32_t)src.scales[r][at] << (8 * b);
-            }
-          }
+          uint64_t v = 0;
+          for (int i = 0; i < blocks; ++i) v |= (uint64_t)src.scales[r][i] << (8 * i);
+          __builtin_memcpy(side.sc[r], &v, (S::kCodes + 3) / 4 * 4);
         }
       }
     }
@@ -429,38 +484,37 @@ struct Stream {
     else asm volatile("s_waitcnt vmcnt(0)" : : : "memory");
   }
 
-  // Streams this workgroup's items (blockIdx.x, + gridDim.x, ...).  Wave w takes chunks
-  // c0 + w, c0 + w + W, ... of a unit (c0 < c1).  at(i): the Source of item i; range(i):
-  // its groups, c0 and c1; done(i, scales): called by all waves after its last chunk, in
-  // order, with acc complete and, row-wise, the rows' scales in LDS.  (The products of
-  // sub-tiles that a shorter unit does not read are of whatever the slot holds, and are
-  // not used.)
-  template <class At, class Range, class Done>
-  __device__ __forceinline__ void run(int items, int wave, f32x4 (&acc)[RT][NT], At at,
-                                      Range range, Done done) const {
-    const int stride = (int)gridDim.x;
+  // Streams this workgroup's items.  A unit's chunks c0, c0 + 1, ... go to the waves in
+  // turn, on from where the unit before it ended.  unit(n): item n of the workgroup, n <
+  // count; at(w): its Source; done(n, w, scales): called by all waves after its last
+  // chunk, in order, with acc complete and, row-wise, the rows' scales in LDS.  (The
+  // products of sub-tiles that a shorter unit does not read are of whatever the slot holds,
+  // and are not used.)
+  template <class Get, class At, class Done>
+  __device__ __forceinline__ void run(int count, int wave, f32x4 (&acc)[RT][NT], Get unit, At at,
+                                      Done done) const {
+    if (count <= 0) return;
     // reading side: the next chunk to issue
-    int ri = (int)blockIdx.x, rn = 0;
-    if (ri >= items) return;
-    Source<RT, NT> rs = at(ri);
+    int rn = 0, turn = 0;                             // turn: the wave of the unit's chunk c0
+    Source<RT, NT> rs = at(unit(0));
     int rc = rs.c0 + wave;
     auto more = [&]() __attribute__((always_inline)) {
-      while (ri < items && (rs.groups == 0 || rc >= rs.c1)) {
-        rn += rs.groups > 0;
-        ri += stride;
-        if (ri < items) {
-          rs = at(ri);
-          rc = rs.c0 + wave;
+      while (rn < count && (rs.groups == 0 || rc >= rs.c1)) {
+        if (rs.groups > 0) turn = (turn + rs.c1 - rs.c0) % W;
+        if (++rn < count) {
+          rs = at(unit(rn));
+          rc = rs.c0 + (wave - turn + W) % W;
         }
       }
-      return ri < items;
+      return rn < count;
     };
     auto read = [&](S& side, int slot) __attribute__((always_inline)) {
-      // Wave 0 copies a unit's row scales ahead of its first chunk, so they have
-      // landed when it multiplies that chunk; the other waves see them after the
-      // first barrier of done().  It runs at most two units ahead of done(), whose
-      // barriers every wave has passed for the unit before: four places suffice.
-      if (MODE == kRowwise && wave == 0 && rc == rs.c0)
+      // The wave of a unit's first chunk copies the row scales ahead of it, so they have
+      // landed when it multiplies that chunk; the other waves see them after the first
+      // barrier of done().  A wave reads at most two units ahead of its done(), whose
+      // barriers every wave has passed for the unit before: four places suffice (places
+      // of empty pieces stay unused).
+      if (MODE == kRowwise && rc == rs.c0)
 #pragma unroll
         for (int i = 0; i < (RT + 3) / 4; ++i)
           __builtin_amdgcn_raw_ptr_buffer_load_lds(
@@ -471,12 +525,16 @@ struct Stream {
       issue(rs, rc, side, slot);
       rc += W;
     };
-    // multiplying side: item mi, `left` chunks of it to come
-    int mi = (int)blockIdx.x, mn = 0, mg = 0, left = 0;
+    // multiplying side: item mn, `left` chunks of it to come
+    int mn = 0, left = 0, mturn = 0;
+    Unit mu;
     auto begin_unit = [&]() __attribute__((always_inline)) {
+      mu = unit(mn);
       int c0, c1;
-      range(mi, &mg, &c0, &c1);
-      left = mg > 0 && c1 - c0 > wave ? (c1 - c0 - wave + W - 1) / W : 0;
+      range(mu.part, &c0, &c1);
+      const int first = (wave - mturn + W) % W;
+      left = mu.groups > 0 && c1 - c0 > first ? (c1 - c0 - first + W - 1) / W : 0;
+      if (mu.groups > 0) mturn = (mturn + c1 - c0) % W;
 #pragma unroll
       for (int r = 0; r < RT; ++r)
 #pragma unroll
@@ -492,9 +550,8 @@ struct Stream {
 #pragma unroll
       for (int b = 0; b < 2; ++b) {
         while (left == 0) {
-          if (mg > 0) done(mi, row_scale[mn++ & 3]);
-          mi += stride;
-          if (mi >= items) return;
+          done(mn, mu, row_scale[mn & 3]);
+          if (++mn >= count) return;
           begin_unit();
         }
         // this chunk's copies have landed: at most the next one's are outstanding
@@ -506,6 +563,13 @@ struct Stream {
         if (more()) read(side[b], b);
       }
     }
+  }
+
+  // Chunks [c0, c1) of part `part` of K.
+  __device__ __forceinline__ void range(int part, int* c0, int* c1) const {
+    const int chunks = (bytes + CH - 1) / CH;
+    *c0 = parts == 1 ? 0 : (int)((int64_t)chunks * part / parts);
+    *c1 = parts == 1 ? chunks : (int)((int64_t)chunks * (part + 1) / parts);
   }
 };
 
@@ -568,6 +632,7 @@ struct Shared {
   float row_scale[4][RT < 4 ? 64 : 16 * RT];
   Partials<W> part;
   Lists l;
+  Units units;
 };
 
 struct Workspace {
@@ -595,23 +660,19 @@ __global__ __launch_bounds__(64 * W, W / 4) void moe_up_kernel(MoeProblem p, Wor
     ws.arrived[i] = 0;
   build_lists(l, reinterpret_cast<int*>(lds.ring), p, 16 * NT);
   const int bytes = row_bytes<FMT>(p.H);
-  const int chunks = (bytes + CH - 1) / CH;
   const Schedule<RT / 2> plan(l, p.I / 16, 1, 16 * NT);
   constexpr int kXGroup = kFrags<FMT> * 16;          // bytes of a lane group's activations
   const float* fs = static_cast<const float*>(p.s13);
-  int ahead = 0, behind = 0, counted = 0;
-  auto range = [&](int u, int* n, int* c0, int* c1) __attribute__((always_inline)) {
-    *n = plan.at(l, u, counted).groups;
-    *c0 = 0;
-    *c1 = chunks;
-  };
-  auto at = [&](int u) __attribute__((always_inline)) {
-    const Unit w = plan.at(l, u, ahead);
+  lds.units.look_up_first(plan, l);
+  const Stream<W, FMT, MODE, X, RT, NT, CH> stream{
+      lds.ring[wave], lds.row_scale,
+      shared_buffer(const_cast<void*>(p.x), (uint32_t)(((p.T - 1) * p.ldx + p.H) * 2)), lane, grp,
+      bytes, 1, p.ld13};
+  auto at = [&](const Unit& w) __attribute__((always_inline)) {
     Source<RT, NT> s;
     s.groups = w.groups;
     s.alone = w.alone;
-    s.c0 = 0;
-    s.c1 = chunks;
+    stream.range(w.part, &s.c0, &s.c1);
     const uint8_t* base = p.w13 + (int64_t)w.e * p.stride13;
     s.row_scale = fs + (int64_t)w.e * 2 * p.I;
 #pragma unroll
@@ -630,13 +691,17 @@ __global__ __launch_bounds__(64 * W, W / 4) void moe_up_kernel(MoeProblem p, Wor
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
       const int c = w.from + 16 * n + (lane & 15);
-      s.col[n] = c < w.last ? l.list[c] / p.k * (int)p.ldx * 2 + grp * kXGroup : kNoColumn;
+      s.col[n] = c < w.last ? l.token[c] * (int)p.ldx * 2 + grp * kXGroup : kNoColumn;
     }
     return s;
   };
   f32x4 acc[RT][NT];
-  auto done = [&](int u, const float* scales) __attribute__((always_inline)) {
-    const Unit w = plan.at(l, u, behind);
+  auto done = [&](int n_item, const Unit& w, const float* scales) __attribute__((always_inline)) {
+    lds.units.look_up_next(plan, l, n_item, wave, W);
+    if (w.groups == 0) {
+      lds_barrier();                  // an item for the waves' order all the same
+      return;
+    }
     const float ts = MODE == kTensor ? uniform_load(fs + w.e) : 1.0f;
     join_waves<W, RT, NT>(lds.part, wave, lane, w.groups, acc, [&](int n, int j) {
       const int c = t / 16, q = t % 16;
@@ -660,11 +725,7 @@ __global__ __launch_bounds__(64 * W, W / 4) void moe_up_kernel(MoeProblem p, Wor
       }
     });
   };
-  const Stream<W, FMT, MODE, X, RT, NT, CH> stream{
-      lds.ring[wave], lds.row_scale,
-      shared_buffer(const_cast<void*>(p.x), (uint32_t)(((p.T - 1) * p.ldx + p.H) * 2)), lane, grp,
-      bytes, p.ld13};
-  stream.run(plan.items, wave, acc, at, range, done);
+  stream.run(plan.count(), wave, acc, [&](int n) { return lds.units.get(n); }, at, done);
 }
 
 // ---------------------------------------------------------------------------
@@ -691,28 +752,20 @@ __global__ __launch_bounds__(64 * W, W / 4) void moe_down_kernel(MoeProblem p, W
     return;
   }
   const int bytes = row_bytes<FMT>(p.I);
-  const int chunks = (bytes + CH - 1) / CH;
   const Schedule<RT / 2> plan(l, groups, ws.splits, 16 * NT);
   constexpr int kXGroup = kFrags<FMT> * 32;
   const __amdgpu_buffer_rsrc_t rp =
       shared_buffer(ws.partial, (uint32_t)((int64_t)ws.splits * pairs * p.H * 4));
   const float* fs = static_cast<const float*>(p.s2);
-  int ahead = 0, behind = 0, counted = 0;
-  auto chunk_range = [&](int part, int* c0, int* c1) {
-    *c0 = (int)((int64_t)chunks * part / ws.splits);
-    *c1 = (int)((int64_t)chunks * (part + 1) / ws.splits);
-  };
-  auto range = [&](int u, int* n, int* c0, int* c1) __attribute__((always_inline)) {
-    const Unit w = plan.at(l, u, counted);
-    *n = w.groups;
-    chunk_range(w.part, c0, c1);
-  };
-  auto at = [&](int u) __attribute__((always_inline)) {
-    const Unit w = plan.at(l, u, ahead);
+  lds.units.look_up_first(plan, l);
+  const Stream<W, FMT, MODE, kXPair, RT, NT, CH> stream{
+      lds.ring[wave], lds.row_scale, shared_buffer(ws.pair, (uint32_t)((int64_t)pairs * p.I * 4)),
+      lane, grp, bytes, ws.splits, p.ld2};
+  auto at = [&](const Unit& w) __attribute__((always_inline)) {
     Source<RT, NT> s;
     s.groups = w.groups;
     s.alone = w.alone;
-    chunk_range(w.part, &s.c0, &s.c1);
+    stream.range(w.part, &s.c0, &s.c1);
     const uint8_t* base = p.w2 + (int64_t)w.e * p.stride2;
     s.row_scale = fs + (int64_t)w.e * p.H;
 #pragma unroll
@@ -736,8 +789,12 @@ __global__ __launch_bounds__(64 * W, W / 4) void moe_down_kernel(MoeProblem p, W
     return s;
   };
   f32x4 acc[RT][NT];
-  auto done = [&](int u, const float* scales) __attribute__((always_inline)) {
-    const Unit w = plan.at(l, u, behind);
+  auto done = [&](int n_item, const Unit& w, const float* scales) __attribute__((always_inline)) {
+    lds.units.look_up_next(plan, l, n_item, wave, W);
+    if (w.groups == 0) {
+      lds_barrier();                  // an item for the waves' order all the same
+      return;
+    }
     const float ts = MODE == kTensor ? uniform_load(fs + w.e) : 1.0f;
     join_waves<W, RT, NT>(lds.part, wave, lane, w.groups, acc, [&](int n, int j) {
 #pragma unroll
@@ -755,10 +812,7 @@ __global__ __launch_bounds__(64 * W, W / 4) void moe_down_kernel(MoeProblem p, W
       }
     });
   };
-  const Stream<W, FMT, MODE, kXPair, RT, NT, CH> stream{
-      lds.ring[wave], lds.row_scale, shared_buffer(ws.pair, (uint32_t)((int64_t)pairs * p.I * 4)),
-      lane, grp, bytes, p.ld2};
-  stream.run(plan.items, wave, acc, at, range, done);
+  stream.run(plan.count(), wave, acc, [&](int n) { return lds.units.get(n); }, at, done);
 
   // A group's rows of out are complete when its positions have all arrived.  Arrivals
   // are counted once per workgroup, after its last unit: a wait for a unit's stores
@@ -772,8 +826,7 @@ __global__ __launch_bounds__(64 * W, W / 4) void moe_down_kernel(MoeProblem p, W
     int group = -1;
     const int64_t i = i0 + (int64_t)(t / (RT / 2)) * gridDim.x;
     if (i < plan.items) {
-      int a = 0;
-      const Unit w = plan.template at<false>(l, (int)i, a);
+      const Unit w = plan.at(l, (int)i);
       if (t % (RT / 2) < w.groups) {
         group = w.group + t % (RT / 2);
         if (__hip_atomic_fetch_add(&ws.arrived[group], 1, __ATOMIC_RELAXED,
