@@ -19,12 +19,28 @@ typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 
 // Activations of fp32 values; exp(-v) overflows to infinity for v < -88, which
-// gives the limit -0.
+// gives the limit -0.  (The reciprocal is within one ulp.)
 __device__ __forceinline__ float layer_activate(float v, int act) {
   if (act == kActRelu) return fmaxf(v, 0.0f);
   if (act == kActGelu) return 0.5f * v * (1.0f + erff(v * 0.70710678118654752f));
-  if (act == kActSilu) return v / (1.0f + __expf(-v));
+  if (act == kActSilu) return v * __builtin_amdgcn_rcpf(1.0f + __expf(-v));
   return v;
+}
+
+// The same on several values with one branch (the activation is the same for all lanes).
+template <int N>
+__device__ __forceinline__ void activate_all(float (&v)[N], int act) {
+  if (act == kActNone) return;
+  if (act == kActRelu) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = layer_activate(v[i], kActRelu);
+  } else if (act == kActGelu) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = layer_activate(v[i], kActGelu);
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = layer_activate(v[i], kActSilu);
+  }
 }
 
 // v = hi + lo to 16 significant bits (relative error at most 2^-17 unless lo

@@ -143,8 +143,13 @@ hipError_t launch_route_as(const RouteProblem& p, hipStream_t stream) {
 // ---------------------------------------------------------------------------
 constexpr int kSortThreads = 1024;
 constexpr int kSortWaves = kSortThreads / 64;
-constexpr int kMaxBlocks = 256;               // blocks of the three-kernel form
-constexpr int kOneBlock = 16384;              // positions that one workgroup sorts alone
+// One workgroup sorts up to 4096 positions alone; up to 64 blocks of 1024 a count kernel
+// and a placement kernel that adds the blocks before its own up; beyond, a kernel of prefix
+// sums between them.  (32768 positions of 8 groups: 13.0 us in three kernels of 4096
+// positions each.)
+constexpr int kOneBlock = 4096;
+constexpr int kShortBlock = 1024, kShortBlocks = 64;
+constexpr int kLongBlock = 4096, kMaxBlocks = 256;
 
 // Group of position i: [0, groups), or `groups` for an id that names none.
 __device__ __forceinline__ int group_of(const int32_t* ids, int i, int groups) {
@@ -244,8 +249,8 @@ __global__ __launch_bounds__(kSortThreads) void sort_one_kernel(const int32_t* i
   place(ids, first, last, groups, bits, next[wave], order);
 }
 
-// Many positions, three kernels: counts[g][block], their prefix sums over the
-// blocks, then the placement.  Blocks are contiguous runs of positions.
+// Many positions: counts[g][block], their prefix sums over the blocks, then the
+// placement.  Blocks are contiguous runs of positions.
 __global__ __launch_bounds__(kSortThreads) void sort_count_kernel(const int32_t* ids, int n,
                                                                   int groups, int span,
                                                                   int32_t* counts) {
@@ -287,6 +292,28 @@ __global__ __launch_bounds__(kSortThreads) void sort_place_kernel(
     const int32_t* totals, int32_t* order, int32_t* offsets) {
   __shared__ int next[kSortWaves][kMaxExperts + 1];
   __shared__ int scratch[kSortWaves];
+  const int blocks = (int)gridDim.x;
+  // positions of group g before this block's, and in all
+  auto before = [&](int g, int* total) {
+    if (totals) {                               // the counts are prefix sums already
+      *total = totals[g];
+      return counts[(int64_t)g * blocks + blockIdx.x];
+    }
+    int sum = 0, mine = 0;
+    for (int b0 = 0; b0 < blocks; b0 += 16) {   // sixteen loads under way at a time
+      int c[16];
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        c[i] = b0 + i < blocks ? counts[(int64_t)g * blocks + b0 + i] : 0;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        mine = b0 + i == (int)blockIdx.x ? sum : mine;
+        sum += c[i];
+      }
+    }
+    *total = sum;
+    return mine;
+  };
   const int t = (int)threadIdx.x, wave = t / 64, lane = t % 64;
   for (int w = 0; w < kSortWaves; ++w)
     for (int g = t; g <= groups; g += kSortThreads) next[w][g] = 0;
@@ -298,8 +325,8 @@ __global__ __launch_bounds__(kSortThreads) void sort_place_kernel(
   const int last = (int)(f + chunk < block1 ? f + chunk : block1);
   for (int i = first + lane; i < last; i += 64) atomicAdd(&next[wave][group_of(ids, i, groups)], 1);
   __syncthreads();
-  int valid;
-  const int total = t < groups ? totals[t] : 0;
+  int valid, total = 0, earlier = 0;
+  if (t < groups) earlier = before(t, &total);
   const int base = exclusive_scan(total, scratch, &valid);
   if (blockIdx.x == 0 && t < groups) offsets[t] = base;
   if (blockIdx.x == 0 && t == 0) offsets[groups] = valid;
@@ -310,9 +337,8 @@ __global__ __launch_bounds__(kSortThreads) void sort_place_kernel(
       at += c;
     }
   };
-  if (t < groups) spread(t, base + counts[(int64_t)t * gridDim.x + blockIdx.x]);
-  if (t == kSortThreads - 1)
-    spread(groups, valid + counts[(int64_t)groups * gridDim.x + blockIdx.x]);
+  if (t < groups) spread(t, base + earlier);
+  if (t == kSortThreads - 1) spread(groups, valid + before(groups, &total));
   __syncthreads();
   place(ids, first, last, groups, bits, next[wave], order);
 }
@@ -321,8 +347,10 @@ __global__ void sort_none_kernel(int32_t* offsets, int groups) {
   for (int g = (int)threadIdx.x; g <= groups; g += (int)blockDim.x) offsets[g] = 0;
 }
 
+bool sort_short(int64_t n) { return n <= kShortBlock * kShortBlocks; }
 int sort_blocks(int64_t n) {
-  const int64_t b = (n + 4095) / 4096;
+  if (sort_short(n)) return (int)((n + kShortBlock - 1) / kShortBlock);
+  const int64_t b = (n + kLongBlock - 1) / kLongBlock;
   return (int)(b < kMaxBlocks ? b : kMaxBlocks);
 }
 
@@ -359,11 +387,12 @@ hipError_t launch_group_rows(const int32_t* ids, int n, int groups, int32_t* ord
     const int blocks = sort_blocks(n);
     const int chunk = up64(((int64_t)n + (int64_t)blocks * kSortWaves - 1) / (blocks * kSortWaves));
     const int span = chunk * kSortWaves;            // blocks past the end have no positions
-    int32_t* totals = workspace + (size_t)(groups + 1) * blocks;
+    int32_t* totals = sort_short(n) ? nullptr : workspace + (size_t)(groups + 1) * blocks;
     hipLaunchKernelGGL(sort_count_kernel, dim3(blocks), dim3(kSortThreads), 0, stream, ids, n,
                        groups, span, workspace);
-    hipLaunchKernelGGL(sort_scan_kernel, dim3(groups + 1), dim3(64), 0, stream, workspace, blocks,
-                       totals);
+    if (totals)
+      hipLaunchKernelGGL(sort_scan_kernel, dim3(groups + 1), dim3(64), 0, stream, workspace, blocks,
+                         totals);
     hipLaunchKernelGGL(sort_place_kernel, dim3(blocks), dim3(kSortThreads), 0, stream, ids, n,
                        groups, bits, span, chunk, workspace, totals, order, offsets);
   }

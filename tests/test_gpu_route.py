@@ -107,7 +107,7 @@ def test_route_strided_rows_and_given_outputs():
     assert empty[0].shape == (0, 4)
 
 
-@pytest.mark.parametrize("n,G", [(1, 1), (1, 1024), (5, 3), (63, 8), (64, 8), (65, 32), (200, 1),
+@pytest.mark.parametrize("n,G", [(1, 1), (1, 1024), (5, 3), (63, 8), (64, 8), (65, 32), (200, 1), (4096, 9), (4097, 9), (65536, 300), (65537, 300),
                                  (1024, 16), (1025, 1024), (5000, 7), (16384, 64), (16385, 64),
                                  (20000, 1024), (70001, 256), (300000, 5)])
 @pytest.mark.parametrize("kind", ["uniform", "skewed", "dropped", "none"])
