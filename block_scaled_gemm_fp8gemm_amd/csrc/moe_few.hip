@@ -128,8 +128,8 @@ __device__ __forceinline__ void build_lists(Lists& l, int* count, const MoeProbl
 // 32 rows; a unit is a tile and one column block.  The workgroups take the units in turn,
 // so neighbouring tiles are read at the same time all over the chip, and the units of
 // one tile's column blocks, eight numbers apart, run together on one XCD: its L2 then
-// serves all but one of them.  What is left after the last whole round is cut finer, into
-// pieces of 1, 2 or NP groups, whichever leaves the busiest workgroup the least.
+// serves all but one of them.  What is left after the last whole round is cut into halves
+// where that leaves the busiest workgroup less.
 struct Unit {
   int e, part, group, groups;        // expert, part of K, first group, how many (0: none)
   int from, last;                    // pairs list[from .. last): the columns
@@ -149,16 +149,7 @@ struct Schedule {
     const int units = (int)l.block[l.used] * parts * tiles;
     const int rest = units % grid;
     whole = units - rest;
-    piece = NP;
-    int least = rest ? NP : 0;
-#pragma unroll
-    for (int m = NP / 2; m >= 1; m /= 2) {
-      const int load = (rest * (NP / m) + grid - 1) / grid * m;
-      if (load < least) {
-        least = load;
-        piece = m;
-      }
-    }
+    piece = 2 * rest <= grid ? NP / 2 : NP;
     items = __builtin_amdgcn_readfirstlane(whole + rest * (NP / piece));
     whole = __builtin_amdgcn_readfirstlane(whole);
     piece = __builtin_amdgcn_readfirstlane(piece);
@@ -728,6 +719,84 @@ __global__ __launch_bounds__(64 * W, W / 4) void moe_up_kernel(MoeProblem p, Wor
   stream.run(plan.count(), wave, acc, [&](int n) { return lds.units.get(n); }, at, done);
 }
 
+// No token has an expert: out is zero.
+template <typename OutT, int kThreads>
+__device__ __forceinline__ void zero_out(const MoeProblem& p) {
+  for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < (int64_t)p.T * (p.H / 4);
+       i += (int64_t)gridDim.x * kThreads) {
+    const float z[4] = {0, 0, 0, 0};
+    store4(static_cast<OutT*>(p.out) + i / (p.H / 4) * p.ldo + i % (p.H / 4) * 4, z);
+  }
+}
+
+// A group's rows of out are complete when its positions have all arrived.  Arrivals
+// are counted once per workgroup, after its last unit: a wait for a unit's stores
+// would also wait for the loads that run ahead of it.  The workgroup that counts a
+// group's last arrival adds the slots' rows up, in slot order.
+// complete: kThreads words of LDS, scratch.
+template <typename OutT, int NP, int kThreads>
+__device__ __forceinline__ void add_slots(const MoeProblem& p, const Workspace& ws,
+                                          const Schedule<NP>& plan, const Lists& l, int* complete,
+                                          __amdgpu_buffer_rsrc_t rp) {
+  OutT* out = static_cast<OutT*>(p.out);
+  const int t = (int)threadIdx.x, pairs = p.T * p.k;
+  const int per_group = (int)l.block[l.used] * ws.splits;
+  __builtin_amdgcn_s_waitcnt(0);                       // this thread's rows stored
+  __syncthreads();                                     // ... and every thread's
+  for (int i0 = (int)blockIdx.x; i0 < plan.items; i0 += (int)gridDim.x * (kThreads / NP)) {
+    int group = -1;
+    const int64_t i = i0 + (int64_t)(t / NP) * gridDim.x;
+    if (i < plan.items) {
+      const Unit w = plan.at(l, (int)i);
+      if (t % NP < w.groups) {
+        group = w.group + t % NP;
+        if (__hip_atomic_fetch_add(&ws.arrived[group], 1, __ATOMIC_RELAXED,
+                                   __HIP_MEMORY_SCOPE_AGENT) != per_group - 1)
+          group = -1;
+      }
+    }
+    complete[t] = group;
+    __syncthreads();
+    for (int c = 0; c < kThreads; ++c) {
+      if (i0 + (int64_t)(c / NP) * gridDim.x >= plan.items) break;
+      const int row0 = complete[c] * 32;
+      if (row0 < 0) continue;
+      for (int o = t; o < p.T * 8; o += kThreads) {
+        const int tok = o / 8, q = row0 + o % 8 * 4;
+        if (q >= p.H) continue;
+        float y[4] = {0, 0, 0, 0};
+        int j = 0, part = 0;                           // slot by slot, part by part
+        while (j < p.k) {                              // four loads under way at a time
+          f32x4 v[4];
+          float wt[4];
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const int at = tok * p.k + j;
+            wt[r] = 0.0f;
+            v[r] = f32x4{0, 0, 0, 0};
+            if (j < p.k && (unsigned)p.ids[at] < (unsigned)p.E) {
+              wt[r] = p.weights[at];
+              v[r] = __builtin_bit_cast(
+                  f32x4, __builtin_amdgcn_raw_buffer_load_b128(
+                             rp, ((part * pairs + at) * p.H + q) * 4, 0, kShared));
+            }
+            if (++part == ws.splits) {
+              part = 0;
+              ++j;
+            }
+          }
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) y[c] += wt[r] * v[r][c];
+        }
+        store4(out + (int64_t)tok * p.ldo + q, y);
+      }
+    }
+    __syncthreads();
+  }
+}
+
 // ---------------------------------------------------------------------------
 // out = sum over slots of w (W2 h): a group is 32 rows of W2; K in parts
 // ---------------------------------------------------------------------------
@@ -742,13 +811,8 @@ __global__ __launch_bounds__(64 * W, W / 4) void moe_down_kernel(MoeProblem p, W
   const int wave = __builtin_amdgcn_readfirstlane(t / 64);
   const int pairs = p.T * p.k;
   build_lists(l, reinterpret_cast<int*>(lds.ring), p, 16 * NT);
-  OutT* out = static_cast<OutT*>(p.out);
-  if (l.used == 0) {                  // no token has an expert
-    for (int64_t i = (int64_t)blockIdx.x * kThreads + t; i < (int64_t)p.T * (p.H / 4);
-         i += (int64_t)gridDim.x * kThreads) {
-      const float z[4] = {0, 0, 0, 0};
-      store4(out + i / (p.H / 4) * p.ldo + i % (p.H / 4) * 4, z);
-    }
+  if (l.used == 0) {
+    zero_out<OutT, kThreads>(p);
     return;
   }
   const int bytes = row_bytes<FMT>(p.I);
@@ -814,53 +878,413 @@ __global__ __launch_bounds__(64 * W, W / 4) void moe_down_kernel(MoeProblem p, W
   };
   stream.run(plan.count(), wave, acc, [&](int n) { return lds.units.get(n); }, at, done);
 
-  // A group's rows of out are complete when its positions have all arrived.  Arrivals
-  // are counted once per workgroup, after its last unit: a wait for a unit's stores
-  // would also wait for the loads that run ahead of it.  The workgroup that counts a
-  // group's last arrival adds the slots' rows up, in slot order.
-  int* complete = reinterpret_cast<int*>(lds.ring);
-  const int per_group = (int)l.block[l.used] * ws.splits;
-  __builtin_amdgcn_s_waitcnt(0);                       // this thread's rows stored
-  __syncthreads();                                     // ... and every thread's
-  for (int i0 = (int)blockIdx.x; i0 < plan.items; i0 += (int)gridDim.x * (2 * kThreads / RT)) {
-    int group = -1;
-    const int64_t i = i0 + (int64_t)(t / (RT / 2)) * gridDim.x;
-    if (i < plan.items) {
-      const Unit w = plan.at(l, (int)i);
-      if (t % (RT / 2) < w.groups) {
-        group = w.group + t % (RT / 2);
-        if (__hip_atomic_fetch_add(&ws.arrived[group], 1, __ATOMIC_RELAXED,
-                                   __HIP_MEMORY_SCOPE_AGENT) != per_group - 1)
-          group = -1;
-      }
-    }
-    complete[t] = group;
-    __syncthreads();
-    for (int c = 0; c < kThreads; ++c) {
-      if (i0 + (int64_t)(c / (RT / 2)) * gridDim.x >= plan.items) break;
-      const int row0 = complete[c] * 32;
-      if (row0 < 0) continue;
-      for (int o = t; o < p.T * 8; o += kThreads) {
-        const int tok = o / 8, q = row0 + o % 8 * 4;
-        if (q >= p.H) continue;
-        float y[4] = {0, 0, 0, 0};
-        for (int j = 0; j < p.k; ++j) {
-          const int at = tok * p.k + j;
-          if ((unsigned)p.ids[at] >= (unsigned)p.E) continue;
-          const float wt = p.weights[at];
-          for (int s = 0; s < ws.splits; ++s) {
-            const f32x4 v = __builtin_bit_cast(
-                f32x4, __builtin_amdgcn_raw_buffer_load_b128(
-                           rp, (int)(((s * pairs + at) * p.H + q) * 4), 0, kShared));
+  add_slots<OutT, RT / 2, kThreads>(p, ws, plan, l, reinterpret_cast<int*>(lds.ring), rp);
+}
+
+// ---------------------------------------------------------------------------
+// Experts with many tokens: wide units
+//
+// The activations of 16 tokens are twice the bytes of 16 rows of codes (four times, as
+// pairs of bf16), so from a few tokens per expert on the kernels above are bound by what a
+// CU draws from L2.  Here the waves of a workgroup split the rows instead of K: a unit is
+// 256 rows, 32 per wave, and the activations of a chunk are copied to LDS once for all of
+// them.  Three slots: while one chunk is multiplied, two are under way.  A wave keeps its
+// rows' sums to itself, so there is nothing to join.
+// ---------------------------------------------------------------------------
+template <int FMT, int MODE, int X, int NT>
+struct Wide {
+  static constexpr bool MX = MODE == kMx32;
+  static constexpr int W = 8, CH = 128, kSteps = CH / kStep;
+  static constexpr int kF = kFrags<FMT>;
+  static constexpr int kXFrag = X == kXPair ? 32 : 16;
+  static constexpr int kH = kXFrag / 16;
+  static constexpr int kXBytes = kSteps * 4 * kF * kXFrag;   // a column's chunk
+  static constexpr int kPieces = kXBytes / 16;               // of a column
+  static constexpr int kXCols = 64 / kPieces;                // columns that one copy covers
+  static constexpr int kXCopies = 16 * NT / kXCols;
+  static constexpr int kXPer = (kXCopies + W - 1) / W;       // copies of a wave
+  static constexpr int kCopies = 4;                          // of a wave's 32 rows
+  static constexpr int kCodes = FMT == kE2M1 ? CH / 16 : CH / 32;
+  static_assert(kPieces <= 64 && kPieces >= 16, "a copy covers whole columns");
+
+  struct Shared {
+    uint8_t ring[3][W][32 * CH];
+    uint8_t x[3][16 * NT * kXBytes];
+    float row_scale[3][32 * W];
+    Lists l;
+    Units units;
+  };
+  // What a wave reads for one unit.
+  struct Source {
+    const uint8_t* codes[2];
+    const uint8_t* scales[2];
+    const float* row_scale;
+    int row_scale_at;
+    int col[kXPer];                  // of this lane's piece of each of its copies
+    int c0, c1, groups;
+    bool alone;
+  };
+  struct Side {
+    uint32_t sc[MX ? 2 : 1][kCodes / 4];
+    int c;
+  };
+
+  Shared& lds;
+  __amdgpu_buffer_rsrc_t x;
+  int wave, lane, grp, bytes, parts;
+  int64_t ld;
+
+  __device__ __forceinline__ void range(int part, int* c0, int* c1) const {
+    const int chunks = (bytes + CH - 1) / CH;
+    *c0 = parts == 1 ? 0 : (int)((int64_t)chunks * part / parts);
+    *c1 = parts == 1 ? chunks : (int)((int64_t)chunks * (part + 1) / parts);
+  }
+
+  // Copy i of this wave: which of the chunk's, its column for this lane and the lane's
+  // piece of it (permuted by the column, so that reads spread over the LDS banks).  Copies
+  // past the last one repeat earlier ones, so that every wave issues as many.
+  __device__ __forceinline__ int copy_index(int i) const { return (i * W + wave) % kXCopies; }
+  __device__ __forceinline__ int copy_column(int i) const {
+    return copy_index(i) * kXCols + lane / kPieces;
+  }
+  __device__ __forceinline__ int copy_piece(int i) const {
+    return (lane % kPieces) ^ (copy_column(i) & 15);
+  }
+
+  __device__ __forceinline__ void issue(const Source& src, int c, Side& side, int slot) const {
+    const bool full = (c + 1) * CH <= bytes;
+    side.c = c;
+    if (wave < src.groups) {
+      if constexpr (MX) {
+        const int blocks = FMT == kE2M1 ? bytes / 16 : bytes / 32;
 #pragma unroll
-            for (int c = 0; c < 4; ++c) y[c] += wt * v[c];
+        for (int r = 0; r < 2; ++r) {
+          if (full) {
+            __builtin_memcpy(side.sc[r], src.scales[r] + c * kCodes, kCodes);
+          } else if (blocks >= kCodes) {               // the row's last codes, moved down
+            uint64_t v = 0;
+            __builtin_memcpy(&v, src.scales[r] + blocks - kCodes, kCodes);
+            v >>= 8 * ((c + 1) * kCodes - blocks);
+            __builtin_memcpy(side.sc[r], &v, kCodes);
+          } else {
+            uint64_t v = 0;
+            for (int i = 0; i < blocks; ++i) v |= (uint64_t)src.scales[r][i] << (8 * i);
+            __builtin_memcpy(side.sc[r], &v, kCodes);
           }
         }
-        store4(out + (int64_t)tok * p.ldo + q, y);
+      }
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const __amdgpu_buffer_rsrc_t rs =
+            __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(src.codes[r]), (short)0,
+                                              0x7fffffff, 0x00020000);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int row = 8 * i + lane / 8;
+          int piece = ((lane % 8) ^ swizzle<CH>(row)) * 16;
+          if (!full && c * CH + piece >= bytes) piece = bytes - 16 - c * CH;
+          uint8_t* dst = lds.ring[slot][wave] + (16 * r + 8 * i) * CH;
+          if (src.alone) copy_to_lds<kNonTemporal>(rs, dst, row * (int)ld + piece, c * CH);
+          else copy_to_lds<0>(rs, dst, row * (int)ld + piece, c * CH);
+        }
       }
     }
-    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kXPer; ++i) {
+      // a piece is (half of) 8 activations, 16 bytes of codes are kF of them
+      const bool past = !full && c * CH + copy_piece(i) / (kF * kH) * 16 >= bytes;
+      copy_to_lds<0>(x, lds.x[slot] + copy_index(i) * 1024, past ? kNoColumn : src.col[i],
+                     c * kXBytes);
+    }
   }
+
+  __device__ __forceinline__ float scale(const Side& side, int r, int s) const {
+    const uint32_t code = FMT == kE2M1 ? (side.sc[r][s] >> (8 * grp)) & 0xffu
+                                       : (side.sc[r][0] >> (16 * s + 8 * (grp >> 1))) & 0xffu;
+    return __uint_as_float(code << 23);
+  }
+
+  __device__ __forceinline__ void multiply(const Side& side, int slot, f32x4 (&acc)[2][NT]) const {
+    const uint8_t* from = lds.ring[slot][wave] + (lane & 15) * CH;
+    const uint8_t* cols = lds.x[slot] + (lane & 15) * kXBytes;
+    const bool full = (side.c + 1) * CH <= bytes;
+#pragma unroll
+    for (int s = 0; s < kSteps; ++s) {
+      u32x4 w[2];
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        w[r] = *reinterpret_cast<const u32x4*>(from + r * 16 * CH +
+                                               ((4 * s + grp) ^ swizzle<CH>(lane & 15)) * 16);
+        if (!full && side.c * CH + s * kStep + grp * 16 >= bytes) w[r] = u32x4{0, 0, 0, 0};
+      }
+#pragma unroll
+      for (int m = 0; m < kF; ++m) {
+        u32x4 a[2];
+#pragma unroll
+        for (int r = 0; r < 2; ++r) a[r] = decode8<FMT, X>(w[r], m, MX ? scale(side, r, s) : 1.0f);
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          u32x4 v[kH];
+#pragma unroll
+          for (int h = 0; h < kH; ++h) {
+            const int piece = ((4 * s + grp) * kF + m) * kH + h;
+            v[h] = *reinterpret_cast<const u32x4*>(cols + n * 16 * kXBytes +
+                                                   (piece ^ (lane & 15)) * 16);
+          }
+          if constexpr (X == kXF16) {
+#pragma unroll
+            for (int r = 0; r < 2; ++r)
+              acc[r][n] = __builtin_amdgcn_mfma_f32_16x16x32_f16(
+                  __builtin_bit_cast(f16x8, a[r]), __builtin_bit_cast(f16x8, v[0]), acc[r][n], 0,
+                  0, 0);
+          } else {
+            bf16x8 hi = __builtin_bit_cast(bf16x8, v[0]), lo{};
+            if constexpr (X == kXPair) lo = __builtin_bit_cast(bf16x8, v[kH - 1]);
+            if constexpr (X == kXF16Split) {
+              const f16x8 f = __builtin_bit_cast(f16x8, v[0]);
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                __bf16 a1, a2;
+                split_bf16((float)f[i], a1, a2);
+                hi[i] = a1;
+                lo[i] = a2;
+              }
+            }
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+              acc[r][n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                  __builtin_bit_cast(bf16x8, a[r]), hi, acc[r][n], 0, 0, 0);
+              if constexpr (X == kXPair || X == kXF16Split)
+                acc[r][n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                    __builtin_bit_cast(bf16x8, a[r]), lo, acc[r][n], 0, 0, 0);
+            }
+          }
+        }
+      }
+    }
+  }
+
+  // Streams this workgroup's `count` items; every wave goes through the same chunks.
+  // at(w): the Source of a unit; done(n, w, scales): called by every wave after item n's
+  // last chunk, with acc its own rows' sums and, row-wise, the unit's row scales in LDS.
+  template <class At, class Done>
+  __device__ __forceinline__ void run(int count, f32x4 (&acc)[2][NT], At at, Done done) const {
+    if (count <= 0) return;
+    // reading side: the next chunk to issue, two chunks ahead at most
+    int rn = 0, rslot = 0;                            // rslot: place of the unit's row scales
+    Source rs = at(lds.units.get(0));
+    int rc = rs.c0;
+    auto more = [&]() __attribute__((always_inline)) {
+      while (rn < count && (rs.groups == 0 || rc >= rs.c1)) {
+        if (rs.groups > 0) rslot = rslot == 2 ? 0 : rslot + 1;
+        if (++rn < count) {
+          rs = at(lds.units.get(rn));
+          rc = rs.c0;
+        }
+      }
+      return rn < count;
+    };
+    int issued[3] = {-1, -1, -1};                     // groups of the chunk in each slot
+    auto read = [&](Side& side, int slot) __attribute__((always_inline)) {
+      // Ahead of a unit's first chunk: half of the waves copy the scales of 64 rows each.
+      // The barriers of every chunk keep all waves within one, so the unit whose place is
+      // taken (three units back) is finished.
+      if (MODE == kRowwise && rc == rs.c0 && wave < W / 2)
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(
+            __builtin_amdgcn_make_buffer_rsrc(const_cast<float*>(rs.row_scale), (short)0,
+                                              0x7fffffff, 0x00020000),
+            (__attribute__((address_space(3))) void*)(lds.row_scale[rslot] + 64 * wave), 4,
+            rs.row_scale_at, 0, 0, 0);
+      issue(rs, rc, side, slot);
+      issued[slot] = rs.groups;
+      ++rc;
+    };
+    int mn = 0, mslot = 0, left = 0;
+    Unit mu;
+    auto begin_unit = [&]() __attribute__((always_inline)) {
+      mu = lds.units.get(mn);
+      int c0, c1;
+      range(mu.part, &c0, &c1);
+      left = mu.groups > 0 ? c1 - c0 : 0;
+#pragma unroll
+      for (int r = 0; r < 2; ++r)
+#pragma unroll
+        for (int n = 0; n < NT; ++n) acc[r][n] = f32x4{0, 0, 0, 0};
+    };
+    Side side[3];
+    if (more()) read(side[0], 0);
+    if (more()) read(side[1], 1);
+    begin_unit();
+    bool ended = false;
+    auto step = [&](auto bt) __attribute__((always_inline)) {
+      constexpr int b = decltype(bt)::value, next = (b + 1) % 3, after = (b + 2) % 3;
+      while (left == 0) {
+        done(mn, mu, lds.row_scale[mslot]);
+        if (mu.groups > 0) mslot = mslot == 2 ? 0 : mslot + 1;
+        if (++mn >= count) {
+          ended = true;
+          return;
+        }
+        begin_unit();
+      }
+      // this wave's copies of the chunk have landed (at most the next chunk's are
+      // outstanding) and its reads of the chunk before are done; then every wave's
+      if (issued[next] < 0) asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" : : : "memory");
+      else if (wave < issued[next])
+        asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" : : "n"(kCopies + kXPer) : "memory");
+      else asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" : : "n"(kXPer) : "memory");
+      asm volatile("s_barrier" : : : "memory");
+      issued[b] = -1;
+      if (more()) read(side[after], after);
+      multiply(side[b], b, acc);
+      --left;
+    };
+    while (!ended) {
+      step(std::integral_constant<int, 0>{});
+      if (ended) break;
+      step(std::integral_constant<int, 1>{});
+      if (ended) break;
+      step(std::integral_constant<int, 2>{});
+    }
+  }
+};
+
+template <int FMT, int MODE, int X, int NT>
+__global__ __launch_bounds__(512, 2) void moe_up_wide_kernel(MoeProblem p, Workspace ws,
+                                                             int down_groups) {
+  using K = Wide<FMT, MODE, X, NT>;
+  __shared__ __attribute__((aligned(1024))) typename K::Shared lds;
+  Lists& l = lds.l;
+  const int t = (int)threadIdx.x, lane = t % 64, grp = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(t / 64);
+  for (int i = (int)blockIdx.x * 512 + t; i < down_groups; i += (int)gridDim.x * 512)
+    ws.arrived[i] = 0;
+  build_lists(l, reinterpret_cast<int*>(lds.ring), p, 16 * NT);
+  const Schedule<8> plan(l, p.I / 16, 1, 16 * NT);
+  lds.units.look_up_first(plan, l);
+  const float* fs = static_cast<const float*>(p.s13);
+  const K k{lds, shared_buffer(const_cast<void*>(p.x), (uint32_t)(((p.T - 1) * p.ldx + p.H) * 2)),
+            wave, lane, grp, row_bytes<FMT>(p.H), 1, p.ld13};
+  auto at = [&](const Unit& w) __attribute__((always_inline)) {
+    typename K::Source s;
+    s.groups = w.groups;
+    s.alone = w.alone;
+    k.range(w.part, &s.c0, &s.c1);
+    s.row_scale = fs + (int64_t)w.e * 2 * p.I;
+    // scales of groups 2 wave and 2 wave + 1: 16 gate rows, their up rows
+    const int sg = 16 * (w.group + 2 * wave + (lane >> 5)) + (lane & 15);
+    s.row_scale_at = 4 * ((lane >> 4 & 1) * p.I + (sg < p.I ? sg : p.I - 1));
+    const int i0 = 16 * (w.group + wave);
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      const int first = r * p.I + (i0 < p.I ? i0 : p.I - 16);
+      s.codes[r] = p.w13 + (int64_t)w.e * p.stride13 + (int64_t)first * p.ld13;
+      const int64_t row = (int64_t)w.e * 2 * p.I + first + (lane & 15);
+      s.scales[r] = MODE == kMx32 ? static_cast<const uint8_t*>(p.s13) + row * (p.H / 32) : nullptr;
+    }
+#pragma unroll
+    for (int i = 0; i < K::kXPer; ++i) {
+      const int c = w.from + k.copy_column(i);
+      s.col[i] = c < w.last ? l.token[c] * (int)p.ldx * 2 + k.copy_piece(i) * 16 : kNoColumn;
+    }
+    return s;
+  };
+  f32x4 acc[2][NT];
+  auto done = [&](int n_item, const Unit& w, const float* scales) __attribute__((always_inline)) {
+    lds.units.look_up_next(plan, l, n_item, wave, 8);
+    if (wave >= w.groups) return;
+    const float ts = MODE == kTensor ? uniform_load(fs + w.e) : 1.0f;
+    f32x4 sg = {ts, ts, ts, ts}, su = sg;
+    if (MODE == kRowwise) {
+      sg = *reinterpret_cast<const f32x4*>(scales + 32 * wave + 4 * grp);
+      su = *reinterpret_cast<const f32x4*>(scales + 32 * wave + 16 + 4 * grp);
+    }
+    const int i = 16 * (w.group + wave) + 4 * grp;    // of I, which is a multiple of 16
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      const int c = w.from + 16 * n + (lane & 15);
+      if (c >= w.last) continue;
+      __bf16 hi[4], lo[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        split_bf16(layer_activate(acc[0][n][j] * sg[j], p.act) * (acc[1][n][j] * su[j]), hi[j],
+                   lo[j]);
+      uint8_t* to = ws.pair + ((int64_t)l.list[c] * p.I + (i & ~7)) * 4 + (i & 7) * 2;
+      __builtin_memcpy(to, hi, 8);
+      __builtin_memcpy(to + 16, lo, 8);
+    }
+  };
+  k.run(plan.count(), acc, at, done);
+}
+
+template <int FMT, int MODE, typename OutT, int NT>
+__global__ __launch_bounds__(512, 2) void moe_down_wide_kernel(MoeProblem p, Workspace ws,
+                                                               int groups) {
+  using K = Wide<FMT, MODE, kXPair, NT>;
+  __shared__ __attribute__((aligned(1024))) typename K::Shared lds;
+  Lists& l = lds.l;
+  const int t = (int)threadIdx.x, lane = t % 64, grp = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(t / 64);
+  const int pairs = p.T * p.k;
+  build_lists(l, reinterpret_cast<int*>(lds.ring), p, 16 * NT);
+  if (l.used == 0) {
+    zero_out<OutT, 512>(p);
+    return;
+  }
+  const Schedule<8> plan(l, groups, ws.splits, 16 * NT);
+  lds.units.look_up_first(plan, l);
+  const float* fs = static_cast<const float*>(p.s2);
+  const __amdgpu_buffer_rsrc_t rp =
+      shared_buffer(ws.partial, (uint32_t)((int64_t)ws.splits * pairs * p.H * 4));
+  const K k{lds, shared_buffer(ws.pair, (uint32_t)((int64_t)pairs * p.I * 4)), wave, lane, grp,
+            row_bytes<FMT>(p.I), ws.splits, p.ld2};
+  auto at = [&](const Unit& w) __attribute__((always_inline)) {
+    typename K::Source s;
+    s.groups = w.groups;
+    s.alone = w.alone;
+    k.range(w.part, &s.c0, &s.c1);
+    s.row_scale = fs + (int64_t)w.e * p.H;
+    const int sn = 32 * w.group + 64 * wave + lane;
+    s.row_scale_at = 4 * (sn < p.H ? sn : p.H - 1);
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      const int n0 = 32 * (w.group + wave) + 16 * r;
+      const int first = n0 < p.H ? n0 : p.H - 16;
+      s.codes[r] = p.w2 + (int64_t)w.e * p.stride2 + (int64_t)first * p.ld2;
+      const int64_t row = (int64_t)w.e * p.H + first + (lane & 15);
+      s.scales[r] = MODE == kMx32 ? static_cast<const uint8_t*>(p.s2) + row * (p.I / 32) : nullptr;
+    }
+#pragma unroll
+    for (int i = 0; i < K::kXPer; ++i) {
+      const int c = w.from + k.copy_column(i);
+      s.col[i] = c < w.last ? l.list[c] * p.I * 4 + k.copy_piece(i) * 16 : kNoColumn;
+    }
+    return s;
+  };
+  f32x4 acc[2][NT];
+  auto done = [&](int n_item, const Unit& w, const float* scales) __attribute__((always_inline)) {
+    lds.units.look_up_next(plan, l, n_item, wave, 8);
+    if (wave >= w.groups) return;
+    const float ts = MODE == kTensor ? uniform_load(fs + w.e) : 1.0f;
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      const int row = 32 * (w.group + wave) + 16 * r + 4 * grp;
+      if (row >= p.H) continue;
+      f32x4 sc = {ts, ts, ts, ts};
+      if (MODE == kRowwise)
+        sc = *reinterpret_cast<const f32x4*>(scales + 32 * wave + 16 * r + 4 * grp);
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        const int c = w.from + 16 * n + (lane & 15);
+        if (c >= w.last) continue;
+        __builtin_amdgcn_raw_buffer_store_b128(
+            __builtin_bit_cast(u32x4, acc[r][n] * sc), rp,
+            (int)(((w.part * pairs + l.list[c]) * p.H + row) * 4), 0, kShared);
+      }
+    }
+  };
+  k.run(plan.count(), acc, at, done);
+  add_slots<OutT, 8, 512>(p, ws, plan, l, reinterpret_cast<int*>(lds.ring), rp);
 }
 
 // ---------------------------------------------------------------------------
@@ -870,22 +1294,35 @@ __global__ __launch_bounds__(64 * W, W / 4) void moe_down_kernel(MoeProblem p, W
 // KiB of LDS, which is what the copies need in flight (units of 32 rows, or of 64 in
 // chunks of 256 bytes by four waves, 3-6 % slower; four waves of 128 rows 20 %).
 constexpr int kW = 8, kRt = 4, kCh = 128;
+constexpr int kWideGroups = 8;       // groups of a wide unit, one per wave
 
 constexpr size_t round256(size_t v) { return (v + 255) / 256 * 256; }
 
 int down_groups(int64_t H) { return (int)((H + 31) / 32); }
 
+// The wide kernels take over from an average of 16 pairs per expert on, of 8 with e2m1
+// codes, whose activations are twice as many.  Narrow and wide, 8 experts of (4096, 14336),
+// top-2, both kernels' time in us (routing with a preference for some experts):
+//   pairs per expert     4          8         16         32
+//   e4m3              235 323    269 333    356 384    563 480
+//   e2m1              183 238    229 261    343 304    580 468
+template <int FMT>
+bool wide(int64_t T, int E, int k) {
+  return T * k > (FMT == kE2M1 ? 8 : 16) * (int64_t)E;
+}
+
 // Parts of the down kernel's K: a unit for every CU at least, where K is long enough to be
-// worth the partial rows.
-int down_splits(int64_t T, int64_t H, int64_t I, int E, int k) {
+// worth the partial rows.  per_unit: groups of 32 rows in a unit.
+int down_splits(int per_unit, int64_t T, int64_t H, int64_t I, int E, int k) {
   const int64_t pairs = T * k;
-  const int64_t units = (down_groups(H) + 1) / 2 * (pairs < E ? pairs : E);
+  const int64_t units = (down_groups(H) + per_unit - 1) / per_unit * (pairs < E ? pairs : E);
   int s = 1;
   while (s < 8 && units * s < 256 && I / (2 * s) >= 1024) s *= 2;
   return s;
 }
 
-Workspace moe_layout(void* base, int64_t T, int64_t H, int64_t I, int E, int k, size_t* total) {
+Workspace moe_layout(void* base, int64_t T, int64_t H, int64_t I, int E, int k, int splits,
+                     size_t* total) {
   Workspace ws;
   uint8_t* b = static_cast<uint8_t*>(base);
   size_t at = kSplitCounterBytes;      // the GEMMs' split-K counters: left alone
@@ -894,34 +1331,34 @@ Workspace moe_layout(void* base, int64_t T, int64_t H, int64_t I, int E, int k, 
   ws.pair = b + at;
   at += round256((size_t)T * k * I * 4);
   ws.partial = reinterpret_cast<float*>(b + at);
-  ws.splits = down_splits(T, H, I, E, k);
-  at += (size_t)ws.splits * T * k * H * 4;
+  ws.splits = splits;
+  at += (size_t)splits * T * k * H * 4;
   *total = at;
   return ws;
 }
 
-template <int FMT, int MODE, int X, typename OutT, int NT>
-hipError_t launch_columns(const MoeProblem& p, hipStream_t stream) {
-  size_t total;
-  const Workspace ws = moe_layout(p.workspace, p.T, p.H, p.I, p.E, p.k, &total);
-  const unsigned cus = (unsigned)device_cu_count();
-  const int groups = down_groups(p.H);
-  hipLaunchKernelGGL((moe_up_kernel<FMT, MODE, X, kW, kRt, NT, kCh>), dim3(cus), dim3(64 * kW), 0,
-                     stream, p, ws, groups);
-  hipLaunchKernelGGL((moe_down_kernel<FMT, MODE, OutT, kW, kRt, NT, kCh>), dim3(cus),
-                     dim3(64 * kW), 0, stream, p, ws, groups);
-  return hipGetLastError();
-}
-
 template <int FMT, int MODE, int X, typename OutT>
 hipError_t launch_as(const MoeProblem& p, hipStream_t stream) {
-  // Column blocks of 32 where an expert has more than 16 pairs on average: E4M3, 8 experts
-  // of 4096 x 14336, two per token: 371 against 372 us at 64 tokens, 527 against 597 at
-  // 128 (292 against 278 at 32).  E2M1 fragments take the registers that these need.
-  if constexpr (FMT != kE2M1)
-    if ((int64_t)p.T * p.k > 16 * (int64_t)p.E)
-      return launch_columns<FMT, MODE, X, OutT, 2>(p, stream);
-  return launch_columns<FMT, MODE, X, OutT, 1>(p, stream);
+  const bool many = wide<FMT>(p.T, p.E, p.k);
+  size_t total;
+  const Workspace ws =
+      moe_layout(p.workspace, p.T, p.H, p.I, p.E, p.k,
+                 down_splits(many ? kWideGroups : kRt / 2, p.T, p.H, p.I, p.E, p.k), &total);
+  const dim3 grid((unsigned)device_cu_count()), block(64 * kW);
+  const int groups = down_groups(p.H);
+  if (many) {
+    // columns of a block: as many as three chunks of them leave room for in LDS
+    hipLaunchKernelGGL((moe_up_wide_kernel<FMT, MODE, X, 2>), grid, block, 0, stream, p, ws,
+                       groups);
+    hipLaunchKernelGGL((moe_down_wide_kernel<FMT, MODE, OutT, FMT == kE2M1 ? 1 : 2>), grid, block,
+                       0, stream, p, ws, groups);
+  } else {
+    hipLaunchKernelGGL((moe_up_kernel<FMT, MODE, X, kW, kRt, 1, kCh>), grid, block, 0, stream, p,
+                       ws, groups);
+    hipLaunchKernelGGL((moe_down_kernel<FMT, MODE, OutT, kW, kRt, 1, kCh>), grid, block, 0, stream,
+                       p, ws, groups);
+  }
+  return hipGetLastError();
 }
 
 template <int FMT, int MODE>
@@ -934,8 +1371,11 @@ hipError_t launch_mode(const MoeProblem& p, hipStream_t stream) {
 }  // namespace
 
 size_t moe_workspace_bytes(int64_t T, int64_t H, int64_t I, int E, int k) {
+  // either form's: which of them runs depends on the format too
+  const int narrow = down_splits(kRt / 2, T, H, I, E, k);
+  const int many = down_splits(kWideGroups, T, H, I, E, k);
   size_t total;
-  moe_layout(nullptr, T, H, I, E, k, &total);
+  moe_layout(nullptr, T, H, I, E, k, narrow > many ? narrow : many, &total);
   return total;
 }
 
