@@ -91,11 +91,14 @@ fp8gemm_status fp8gemm_group_rows(const int32_t* ids, int64_t n, int32_t groups,
 /*         w2 + e*stride2, pitch ld2.  Both E4M3 (any scale mode) or E2M1 (MX32,    */
 /*         two codes per byte).  Layouts of codes and scales as the B operand of    */
 /*         fp8gemm_grouped_run (scale13: [E], [E*2I] or [E][2I][H/32]; scale2: [E],  */
-/*         [E*H] or [E][H][I/32]), so one set of weights serves both calls.  An MX   */
-/*         code of 0 (2^-127) is read as zero.                                    */
-/*   H, I: multiples of 16 (32 with MX32) and H of 8.                             */
+/*         [E*H] or [E][H][I/32]), so one set of weights serves both calls.         */
+/*   H and I: multiples of 16 (32 with MX32), so that codes are whole 16-byte       */
+/*         pieces.                                                                */
 /* 0 <= T <= FP8GEMM_MOE_MAX_TOKENS (more: NOT_SUPPORTED; the grouped GEMM serves    */
 /* longer batches), 1 <= k <= FP8GEMM_MAX_TOP_K, experts <= FP8GEMM_MAX_EXPERTS.      */
+/* Also NOT_SUPPORTED: H, I or a row pitch of codes of 2^27 or more, x or the workspace */
+/* of more than 0x70000000 bytes (32-bit offsets inside them; the expert tensors may    */
+/* have any size).                                                                */
 /*   workspace: fp8gemm_moe_workspace_size() bytes, 16-byte aligned; scratch whose   */
 /*         first 4 KiB stay untouched (a workspace of fp8gemm_run may be shared by    */
 /*         calls that run one after another).                                       */

@@ -170,6 +170,40 @@ def test_mx_scales_over_the_range():
         layer.check((x.float() * 2 ** -6).half(), ids, w * 2.0 ** -12, "relu")
 
 
+@pytest.mark.parametrize("mode,fmt", FORMS)
+@pytest.mark.parametrize("T,H,I,E,k", [(128, 1120, 544, 64, 16), (128, 32, 2080, 100, 16),
+                                       (128, 2080, 32, 100, 16), (120, 512, 1024, 56, 8)])
+def test_many_tokens_over_many_experts(mode, fmt, T, H, I, E, k):
+    """More units than CUs, some with one chunk of K, experts with one column block or more."""
+    layer = Layer(H, I, E, mode, fmt, seed=E + k)
+    layer.check(*layer.inputs(T, k, "f16" if fmt == "e2m1" else "bf16"))
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "e2m1"])
+@pytest.mark.parametrize("T", [1, 128])
+def test_mx_codes_at_the_ends(fmt, T):
+    """Code c is 2^(c - 127), the smallest included, and 255 is NaN: sums of equal powers of
+    two, exact in every step."""
+    H, I = 128, 64
+    one, per = (0x38, 1) if fmt == "e4m3" else (0x22, 2)
+    w13 = torch.full((1, 2 * I, H // per), one, dtype=torch.uint8, device=DEV)
+    w2 = torch.full((1, H, I // per), one, dtype=torch.uint8, device=DEV)
+    ids = torch.zeros((T, 1), dtype=torch.int32, device=DEV)
+    weights = torch.ones((T, 1), device=DEV)
+    x = torch.full((T, H), 2.0 ** 30, dtype=torch.bfloat16, device=DEV)
+    s13 = torch.full((1, 2 * I, H // 32), 120, dtype=torch.uint8, device=DEV)   # g = u = 2^30
+    s2 = torch.full((1, H, I // 32), 127, dtype=torch.uint8, device=DEV)
+    for code in (0, 1, 2, 254 - 127, 255):
+        announce("moe mx code", fmt, T, code)
+        s2[0, :16] = code
+        out = F.moe_experts(x, ids, weights, w13, s13, w2, s2, "mx32", fmt, "relu").double()
+        want = float("nan") if code == 255 else 64 * 2.0 ** 60 * 2.0 ** (code - 127)
+        assert torch.equal(out[:, :16].cpu(),
+                           torch.full((T, 16), want, dtype=torch.float64)) or (
+            code == 255 and bool(out[:, :16].isnan().all()))
+        assert bool((out[:, 16:] == 64 * 2.0 ** 60).all())
+
+
 def test_zero_and_one_tokens_and_determinism():
     layer = Layer(512, 768, 8, "mx32", "e2m1", seed=19)
     x, ids, w = layer.inputs(7, 2, "bf16")
