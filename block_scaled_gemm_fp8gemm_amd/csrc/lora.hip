@@ -104,6 +104,7 @@ constexpr int kShrinkRows = 32;        // rows of x in a tile: two sub-tiles of 
 constexpr int kLine = 128;             // bytes of a row in one chunk
 
 constexpr int kNonTemporal = 2;        // cache policy: rows of x are read once
+
 // Adapter fragments of a chunk: two steps of 32 elements of K.
 template <int NT>
 struct Fragments {
@@ -113,10 +114,13 @@ struct Fragments {
 // A tile of rows of x times NT tiles of 16 adapter rows (from r0 on).  The rows of x are
 // the long operand: they are copied to LDS in whole lines, two slots per wave, the
 // next chunk under way while one is multiplied; wave w takes chunks w, w + 8, ... of the
-// workgroup's part of K.  The adapter's rows come from L2 into registers.
+// workgroup's part of K.  The adapter's rows come from L2 into registers: at rank 64 twice
+// the bytes of the 32 rows of x, which is what bounds it (8192 rows of 4096, 8 adapters:
+// 26 us, 2.6 TB/s of x and 7.7 in all; 64 rows a tile in two parts of K 26, four waves with
+// two workgroups on a CU 28).
 template <typename T, int NT>
-__global__ __launch_bounds__(kShrinkThreads, NT == 4 ? 2 : 4) void lora_shrink_kernel(LoraProblem p, float* v,
-                                                                       int splits, int rblocks) {
+__global__ __launch_bounds__(kShrinkThreads, NT == 4 ? 2 : 4) void lora_shrink_kernel(
+    LoraProblem p, float* v, int splits, int rblocks) {
   // a wave's ring also takes its sums, when its last chunk has been multiplied
   union Ring {
     uint8_t slot[2][kShrinkRows * kLine];
@@ -246,7 +250,8 @@ constexpr int kExpandCols = 64 * (kExpandThreads / 64);   // output columns of a
 // A tile of 16 * MT rows times `run` column blocks; a wave takes 64 columns of each.  v is
 // fetched and split once; the rows of base for the next column block are on their way
 // while one is computed.  The products pass through LDS, so that base is read and out
-// written in whole 128-byte lines.  KS steps of 32 cover the rank.
+// written in whole 128-byte lines.  KS steps of 32 cover the rank.  Bound by base and out:
+// 8192 x 4096, rank 64, 43 us, 134 MB at 3.1 TB/s.
 template <typename T, int KS, int MT>
 __global__ __launch_bounds__(kExpandThreads, 2) void lora_expand_kernel(LoraProblem p,
                                                                      const float* v, int splits,

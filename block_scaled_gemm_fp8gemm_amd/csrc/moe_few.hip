@@ -25,6 +25,11 @@
 //     the same bits on every run.
 // Both kernels are persistent: every workgroup derives the experts in use and their
 // slots from the ids, so the host never reads them.
+//
+// 8 experts of (4096, 14336), top-2, e4m3: one token 46 + 28 us for 235 and 117 MB of codes
+// (5.1 and 4.2 TB/s; a copy reaches 5.2, a plain stream of such tiles 6.7 to 7.0, the rest is
+// the start: lists, units and the first chunk's way from HBM, 5 us a kernel), 16 tokens
+// 141 + 81 us for 940 and 470 MB (6.7 and 5.8 TB/s).
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -133,7 +138,6 @@ __device__ __forceinline__ void build_lists(Lists& l, int* count, const MoeProbl
 struct Unit {
   int e, part, group, groups;        // expert, part of K, first group, how many (0: none)
   int from, last;                    // pairs list[from .. last): the columns
-  bool alone;                        // the tile's only column block
 };
 
 template <int NP>
@@ -199,7 +203,6 @@ struct Schedule {
     w.from = l.start[a] + block * cols;
     const int last = l.start[a + 1];
     w.last = w.from + cols < last ? w.from + cols : last;
-    w.alone = blocks == 1;
     return w;
   }
 };
@@ -219,7 +222,6 @@ struct Units {
     w.groups = __builtin_amdgcn_readfirstlane(v.groups);
     w.from = __builtin_amdgcn_readfirstlane(v.from);
     w.last = __builtin_amdgcn_readfirstlane(v.last);
-    w.alone = __builtin_amdgcn_readfirstlane(v.alone);
     return w;
   }
   template <int NP>
@@ -294,7 +296,6 @@ struct Source {
   int col[NT];                        // byte offset of this lane's column of activations, from
                                       // its lane group's first element on
   int c0, c1;                         // chunks of K
-  bool alone;                         // no other unit reads these rows
   int groups;                         // sub-tiles 2 * groups and more are not read
 };
 
@@ -306,14 +307,15 @@ struct Side {
   static constexpr int kXFrag = X == kXPair ? 32 : 16;      // bytes of 8 activations
   static constexpr int kCodes = FMT == kE2M1 ? CH / 16 : CH / 32;   // MX scale codes of a row
   static_assert(kCodes == 4 || kCodes == 8, "one or two words");
-  uint32_t sc[MX ? RT : 1][(kCodes + 3) / 4];
+  uint32_t sc[MX ? RT : 1][kCodes / 4];
   u32x4 x[kSteps][NT][kF][kXFrag / 16];
   int c;                                                    // which chunk
-  int groups;
+  bool live;                                                // issued and not multiplied
 };
 
-// 16 bytes per lane from a buffer to LDS (lane i to dst + 16 i).  Rows that one unit alone
-// reads take the non-temporal hint (7.0 against 6.3 TB/s in a plain stream of tiles).
+// 16 bytes per lane from a buffer to LDS (lane i to dst + 16 i).  The
+// non-temporal hint is for rows that one unit reads (7.0 against 6.3 TB/s in a plain stream of
+// tiles).
 constexpr int kNonTemporal = 2;
 template <int AUX>
 __device__ __forceinline__ void copy_to_lds(__amdgpu_buffer_rsrc_t rs, uint8_t* dst, int voff,
@@ -329,13 +331,39 @@ __device__ __forceinline__ int swizzle(int r) {
   return CH == 256 ? r & 15 : (r >> 1) & 7;
 }
 
-template <int W, int FMT, int MODE, int X, int RT, int NT, int CH>
+// The N MX scale codes of chunk c of a row that has `blocks` of them, in one load without a
+// branch: at the row's end the last N, which shift_codes moves down when they are used.
+template <int N>
+__device__ __forceinline__ void load_codes(const uint8_t* row, int c, int blocks,
+                                           uint32_t (&sc)[N / 4]) {
+  if (blocks >= N) {
+    const int at = c * N < blocks - N ? c * N : blocks - N;
+    __builtin_memcpy(sc, row + at, N);
+  } else {
+    uint64_t v = 0;
+    for (int i = 0; i < blocks; ++i) v |= (uint64_t)row[i] << (8 * i);
+    __builtin_memcpy(sc, &v, N);
+  }
+}
+template <int N>
+__device__ __forceinline__ void shift_codes(uint32_t (&sc)[N / 4], int c, int blocks) {
+  const int past = blocks >= N && c * N > blocks - N ? 8 * (c * N - (blocks - N)) : 0;
+  if constexpr (N == 4) {
+    sc[0] >>= past;
+  } else {
+    const uint64_t v = (sc[0] | (uint64_t)sc[1] << 32) >> past;
+    sc[0] = (uint32_t)v;
+    sc[1] = (uint32_t)(v >> 32);
+  }
+}
+
+template <int W, int FMT, int MODE, int X, int RT, int NT, int CH, int AUX>
 struct Stream {
   static constexpr bool MX = MODE == kMx32;
   using S = Side<FMT, MX, X, RT, NT, CH>;
   static constexpr int kSlot = RT * 16 * CH;          // bytes of a chunk's codes
   static constexpr int kRowsPer = 1024 / CH;          // rows that one copy covers
-  static constexpr int kCopies = 2 * 16 / kRowsPer;   // copies of a group's rows
+  static constexpr int kCopies = RT * 16 / kRowsPer;  // copies of a chunk
   uint8_t* ring;                                      // this wave's two slots
   float (*row_scale)[RT < 4 ? 64 : 16 * RT];          // row-wise: the rows' scales, by unit
   __amdgpu_buffer_rsrc_t x;                           // the activations
@@ -346,7 +374,7 @@ struct Stream {
   __device__ __forceinline__ void issue(const Source<RT, NT>& src, int c, S& side, int slot) const {
     const bool full = (c + 1) * CH <= bytes;
     side.c = c;
-    side.groups = src.groups;
+    side.live = true;
     constexpr int kXStep = 4 * S::kF * S::kXFrag;     // of a step: four lane groups
 #pragma unroll
     for (int s = 0; s < S::kSteps; ++s) {
@@ -365,39 +393,28 @@ struct Stream {
       }
     }
     if constexpr (MX) {
-      const int blocks = FMT == kE2M1 ? bytes / 16 : bytes / 32;
 #pragma unroll
-      for (int r = 0; r < RT; ++r) {
-        if (full) {
-          __builtin_memcpy(side.sc[r], src.scales[r] + c * S::kCodes, S::kCodes);
-        } else if (blocks >= S::kCodes) {             // the row's last codes, moved down
-          uint64_t v = 0;
-          __builtin_memcpy(&v, src.scales[r] + blocks - S::kCodes, S::kCodes);
-          v >>= 8 * ((c + 1) * S::kCodes - blocks);
-          __builtin_memcpy(side.sc[r], &v, (S::kCodes + 3) / 4 * 4);
-        } else {
-          uint64_t v = 0;
-          for (int i = 0; i < blocks; ++i) v |= (uint64_t)src.scales[r][i] << (8 * i);
-          __builtin_memcpy(side.sc[r], &v, (S::kCodes + 3) / 4 * 4);
-        }
-      }
+      for (int r = 0; r < RT; ++r)
+        load_codes<S::kCodes>(src.scales[r], c, FMT == kE2M1 ? bytes / 16 : bytes / 32,
+                              side.sc[r]);
     }
+    // Every chunk is as many copies, without a branch among them: otherwise the compiler,
+    // which counts the loads that surely follow those of the activations, has the products
+    // wait for the copies too.  Sub-tiles that are not read have a buffer of no bytes.
     uint8_t* to = ring + slot * kSlot;
 #pragma unroll
     for (int r = 0; r < RT; ++r) {
-      if (r / 2 >= src.groups) break;
-      const __amdgpu_buffer_rsrc_t rs =
-          __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(src.codes[r]), (short)0,
-                                            0x7fffffff, 0x00020000);
+      const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
+          const_cast<uint8_t*>(src.codes[r]), (short)0, r / 2 < src.groups ? 0x7fffffff : 0,
+          0x00020000);
 #pragma unroll
       for (int i = 0; i < 16 / kRowsPer; ++i) {
         const int row = i * kRowsPer + lane / (CH / 16);
         int piece = ((lane % (CH / 16)) ^ swizzle<CH>(row)) * 16;
         // past the row's end: its last piece; the product takes zeros instead
         if (!full && c * CH + piece >= bytes) piece = bytes - 16 - c * CH;
-        uint8_t* dst = to + (r * 16 + i * kRowsPer) * CH;
-        if (src.alone) copy_to_lds<kNonTemporal>(rs, dst, row * (int)ld + piece, c * CH);
-        else copy_to_lds<0>(rs, dst, row * (int)ld + piece, c * CH);
+        copy_to_lds<AUX>(rs, to + (r * 16 + i * kRowsPer) * CH, row * (int)ld + piece,
+                         c * CH);
       }
     }
   }
@@ -411,7 +428,12 @@ struct Stream {
     return __uint_as_float(code << 23);
   }
 
-  __device__ __forceinline__ void multiply(const S& side, int slot, f32x4 (&acc)[RT][NT]) const {
+  __device__ __forceinline__ void multiply(S& side, int slot, f32x4 (&acc)[RT][NT]) const {
+    if constexpr (MX) {
+#pragma unroll
+      for (int r = 0; r < RT; ++r)
+        shift_codes<S::kCodes>(side.sc[r], side.c, FMT == kE2M1 ? bytes / 16 : bytes / 32);
+    }
     const uint8_t* from = ring + slot * kSlot + (lane & 15) * CH;
     const bool full = (side.c + 1) * CH <= bytes;
 #pragma unroll
@@ -465,14 +487,11 @@ struct Stream {
     }
   }
 
-  // Waits until at most the copies of `groups` groups are outstanding.
-  __device__ __forceinline__ static void wait_copies(int groups) {
-    static_assert(RT == 2 || RT == 4 || RT == 8, "groups of a unit");
-    if (RT >= 8 && groups == 4) asm volatile("s_waitcnt vmcnt(%0)" : : "n"(4 * kCopies) : "memory");
-    else if (RT >= 8 && groups == 3) asm volatile("s_waitcnt vmcnt(%0)" : : "n"(3 * kCopies) : "memory");
-    else if (RT >= 4 && groups == 2) asm volatile("s_waitcnt vmcnt(%0)" : : "n"(2 * kCopies) : "memory");
-    else if (groups == 1) asm volatile("s_waitcnt vmcnt(%0)" : : "n"(kCopies) : "memory");
-    else asm volatile("s_waitcnt vmcnt(0)" : : : "memory");
+  // Waits until at most the loads of one chunk are outstanding, its activations and its
+  // copies.  (With MX codes there are a few more, so a few of them are waited for.)
+  __device__ __forceinline__ static void wait_next() {
+    constexpr int kX = S::kSteps * NT * S::kF * (S::kXFrag / 16);
+    asm volatile("s_waitcnt vmcnt(%0)" : : "n"(kX + kCopies) : "memory");
   }
 
   // Streams this workgroup's items.  A unit's chunks c0, c0 + 1, ... go to the waves in
@@ -532,7 +551,7 @@ struct Stream {
         for (int n = 0; n < NT; ++n) acc[r][n] = f32x4{0, 0, 0, 0};
     };
     S side[2];
-    side[0].groups = side[1].groups = 0;              // 0: nothing issued
+    side[0].live = side[1].live = false;
 #pragma unroll
     for (int b = 0; b < 2; ++b)
       if (more()) read(side[b], b);
@@ -545,11 +564,12 @@ struct Stream {
           if (++mn >= count) return;
           begin_unit();
         }
-        // this chunk's copies have landed: at most the next one's are outstanding
-        wait_copies(side[b ^ 1].groups);
+        // this chunk's loads have landed: at most the next one's are outstanding
+        if (side[b ^ 1].live) wait_next();
+        else asm volatile("s_waitcnt vmcnt(0)" : : : "memory");
         multiply(side[b], b, acc);
         --left;
-        side[b].groups = 0;
+        side[b].live = false;
         asm volatile("s_waitcnt lgkmcnt(0)" : : : "memory");   // the slot has been read
         if (more()) read(side[b], b);
       }
@@ -637,7 +657,7 @@ struct Workspace {
 // h = act(Wg x) * (Wu x): a group is 16 gate rows (sub-tile 2 j) and their up rows
 // (sub-tile 2 j + 1)
 // ---------------------------------------------------------------------------
-template <int FMT, int MODE, int X, int W, int RT, int NT, int CH>
+template <int FMT, int MODE, int X, int W, int RT, int NT, int CH, int AUX>
 __global__ __launch_bounds__(64 * W, W / 4) void moe_up_kernel(MoeProblem p, Workspace ws,
                                                                int down_groups) {
   constexpr bool kMx = MODE == kMx32;
@@ -655,14 +675,13 @@ __global__ __launch_bounds__(64 * W, W / 4) void moe_up_kernel(MoeProblem p, Wor
   constexpr int kXGroup = kFrags<FMT> * 16;          // bytes of a lane group's activations
   const float* fs = static_cast<const float*>(p.s13);
   lds.units.look_up_first(plan, l);
-  const Stream<W, FMT, MODE, X, RT, NT, CH> stream{
+  const Stream<W, FMT, MODE, X, RT, NT, CH, AUX> stream{
       lds.ring[wave], lds.row_scale,
       shared_buffer(const_cast<void*>(p.x), (uint32_t)(((p.T - 1) * p.ldx + p.H) * 2)), lane, grp,
       bytes, 1, p.ld13};
   auto at = [&](const Unit& w) __attribute__((always_inline)) {
     Source<RT, NT> s;
     s.groups = w.groups;
-    s.alone = w.alone;
     stream.range(w.part, &s.c0, &s.c1);
     const uint8_t* base = p.w13 + (int64_t)w.e * p.stride13;
     s.row_scale = fs + (int64_t)w.e * 2 * p.I;
@@ -800,7 +819,7 @@ __device__ __forceinline__ void add_slots(const MoeProblem& p, const Workspace& 
 // ---------------------------------------------------------------------------
 // out = sum over slots of w (W2 h): a group is 32 rows of W2; K in parts
 // ---------------------------------------------------------------------------
-template <int FMT, int MODE, typename OutT, int W, int RT, int NT, int CH>
+template <int FMT, int MODE, typename OutT, int W, int RT, int NT, int CH, int AUX>
 __global__ __launch_bounds__(64 * W, W / 4) void moe_down_kernel(MoeProblem p, Workspace ws,
                                                                  int groups) {
   constexpr bool kMx = MODE == kMx32;
@@ -822,13 +841,12 @@ __global__ __launch_bounds__(64 * W, W / 4) void moe_down_kernel(MoeProblem p, W
       shared_buffer(ws.partial, (uint32_t)((int64_t)ws.splits * pairs * p.H * 4));
   const float* fs = static_cast<const float*>(p.s2);
   lds.units.look_up_first(plan, l);
-  const Stream<W, FMT, MODE, kXPair, RT, NT, CH> stream{
+  const Stream<W, FMT, MODE, kXPair, RT, NT, CH, AUX> stream{
       lds.ring[wave], lds.row_scale, shared_buffer(ws.pair, (uint32_t)((int64_t)pairs * p.I * 4)),
       lane, grp, bytes, ws.splits, p.ld2};
   auto at = [&](const Unit& w) __attribute__((always_inline)) {
     Source<RT, NT> s;
     s.groups = w.groups;
-    s.alone = w.alone;
     stream.range(w.part, &s.c0, &s.c1);
     const uint8_t* base = p.w2 + (int64_t)w.e * p.stride2;
     s.row_scale = fs + (int64_t)w.e * p.H;
@@ -922,7 +940,6 @@ struct Wide {
     int row_scale_at;
     int col[kXPer];                  // of this lane's piece of each of its copies
     int c0, c1, groups;
-    bool alone;
   };
   struct Side {
     uint32_t sc[MX ? 2 : 1][kCodes / 4];
@@ -954,39 +971,25 @@ struct Wide {
   __device__ __forceinline__ void issue(const Source& src, int c, Side& side, int slot) const {
     const bool full = (c + 1) * CH <= bytes;
     side.c = c;
-    if (wave < src.groups) {
-      if constexpr (MX) {
-        const int blocks = FMT == kE2M1 ? bytes / 16 : bytes / 32;
+    if constexpr (MX) {
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          if (full) {
-            __builtin_memcpy(side.sc[r], src.scales[r] + c * kCodes, kCodes);
-          } else if (blocks >= kCodes) {               // the row's last codes, moved down
-            uint64_t v = 0;
-            __builtin_memcpy(&v, src.scales[r] + blocks - kCodes, kCodes);
-            v >>= 8 * ((c + 1) * kCodes - blocks);
-            __builtin_memcpy(side.sc[r], &v, kCodes);
-          } else {
-            uint64_t v = 0;
-            for (int i = 0; i < blocks; ++i) v |= (uint64_t)src.scales[r][i] << (8 * i);
-            __builtin_memcpy(side.sc[r], &v, kCodes);
-          }
-        }
-      }
+      for (int r = 0; r < 2; ++r)
+        load_codes<kCodes>(src.scales[r], c, FMT == kE2M1 ? bytes / 16 : bytes / 32, side.sc[r]);
+    }
+    // no branch among the copies, as above: a wave past the unit's groups copies from a buffer
+    // of no bytes, and rows that several units read are not told apart (no hint)
 #pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        const __amdgpu_buffer_rsrc_t rs =
-            __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(src.codes[r]), (short)0,
-                                              0x7fffffff, 0x00020000);
+    for (int r = 0; r < 2; ++r) {
+      const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
+          const_cast<uint8_t*>(src.codes[r]), (short)0, wave < src.groups ? 0x7fffffff : 0,
+          0x00020000);
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int row = 8 * i + lane / 8;
-          int piece = ((lane % 8) ^ swizzle<CH>(row)) * 16;
-          if (!full && c * CH + piece >= bytes) piece = bytes - 16 - c * CH;
-          uint8_t* dst = lds.ring[slot][wave] + (16 * r + 8 * i) * CH;
-          if (src.alone) copy_to_lds<kNonTemporal>(rs, dst, row * (int)ld + piece, c * CH);
-          else copy_to_lds<0>(rs, dst, row * (int)ld + piece, c * CH);
-        }
+      for (int i = 0; i < 2; ++i) {
+        const int row = 8 * i + lane / 8;
+        int piece = ((lane % 8) ^ swizzle<CH>(row)) * 16;
+        if (!full && c * CH + piece >= bytes) piece = bytes - 16 - c * CH;
+        copy_to_lds<0>(rs, lds.ring[slot][wave] + (16 * r + 8 * i) * CH, row * (int)ld + piece,
+                       c * CH);
       }
     }
 #pragma unroll
@@ -1004,7 +1007,12 @@ struct Wide {
     return __uint_as_float(code << 23);
   }
 
-  __device__ __forceinline__ void multiply(const Side& side, int slot, f32x4 (&acc)[2][NT]) const {
+  __device__ __forceinline__ void multiply(Side& side, int slot, f32x4 (&acc)[2][NT]) const {
+    if constexpr (MX) {
+#pragma unroll
+      for (int r = 0; r < 2; ++r)
+        shift_codes<kCodes>(side.sc[r], side.c, FMT == kE2M1 ? bytes / 16 : bytes / 32);
+    }
     const uint8_t* from = lds.ring[slot][wave] + (lane & 15) * CH;
     const uint8_t* cols = lds.x[slot] + (lane & 15) * kXBytes;
     const bool full = (side.c + 1) * CH <= bytes;
@@ -1084,7 +1092,7 @@ struct Wide {
       }
       return rn < count;
     };
-    int issued[3] = {-1, -1, -1};                     // groups of the chunk in each slot
+    bool issued[3] = {false, false, false};
     auto read = [&](Side& side, int slot) __attribute__((always_inline)) {
       // Ahead of a unit's first chunk: half of the waves copy the scales of 64 rows each.
       // The barriers of every chunk keep all waves within one, so the unit whose place is
@@ -1096,7 +1104,7 @@ struct Wide {
             (__attribute__((address_space(3))) void*)(lds.row_scale[rslot] + 64 * wave), 4,
             rs.row_scale_at, 0, 0, 0);
       issue(rs, rc, side, slot);
-      issued[slot] = rs.groups;
+      issued[slot] = true;
       ++rc;
     };
     int mn = 0, mslot = 0, left = 0;
@@ -1129,12 +1137,12 @@ struct Wide {
       }
       // this wave's copies of the chunk have landed (at most the next chunk's are
       // outstanding) and its reads of the chunk before are done; then every wave's
-      if (issued[next] < 0) asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" : : : "memory");
-      else if (wave < issued[next])
+      if (issued[next])
         asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" : : "n"(kCopies + kXPer) : "memory");
-      else asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" : : "n"(kXPer) : "memory");
+      else
+        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" : : : "memory");
       asm volatile("s_barrier" : : : "memory");
-      issued[b] = -1;
+      issued[b] = false;
       if (more()) read(side[after], after);
       multiply(side[b], b, acc);
       --left;
@@ -1168,7 +1176,6 @@ __global__ __launch_bounds__(512, 2) void moe_up_wide_kernel(MoeProblem p, Works
   auto at = [&](const Unit& w) __attribute__((always_inline)) {
     typename K::Source s;
     s.groups = w.groups;
-    s.alone = w.alone;
     k.range(w.part, &s.c0, &s.c1);
     s.row_scale = fs + (int64_t)w.e * 2 * p.I;
     // scales of groups 2 wave and 2 wave + 1: 16 gate rows, their up rows
@@ -1241,7 +1248,6 @@ __global__ __launch_bounds__(512, 2) void moe_down_wide_kernel(MoeProblem p, Wor
   auto at = [&](const Unit& w) __attribute__((always_inline)) {
     typename K::Source s;
     s.groups = w.groups;
-    s.alone = w.alone;
     k.range(w.part, &s.c0, &s.c1);
     s.row_scale = fs + (int64_t)w.e * p.H;
     const int sn = 32 * w.group + 64 * wave + lane;
@@ -1352,12 +1358,24 @@ hipError_t launch_as(const MoeProblem& p, hipStream_t stream) {
                        groups);
     hipLaunchKernelGGL((moe_down_wide_kernel<FMT, MODE, OutT, FMT == kE2M1 ? 1 : 2>), grid, block,
                        0, stream, p, ws, groups);
-  } else {
-    hipLaunchKernelGGL((moe_up_kernel<FMT, MODE, X, kW, kRt, 1, kCh>), grid, block, 0, stream, p,
-                       ws, groups);
-    hipLaunchKernelGGL((moe_down_kernel<FMT, MODE, OutT, kW, kRt, 1, kCh>), grid, block, 0, stream,
-                       p, ws, groups);
+    return hipGetLastError();
   }
+  // Rows that mostly one column block reads take the non-temporal hint; with more than 8 pairs
+  // per expert on average the preferred experts have two (16: 386 us with the hint on every
+  // copy, 353 without).
+  auto launch = [&](auto aux) {
+    constexpr int kAux = decltype(aux)::value;
+    hipLaunchKernelGGL((moe_up_kernel<FMT, MODE, X, kW, kRt, 1, kCh, kAux>), grid, block, 0, stream,
+                       p, ws, groups);
+    hipLaunchKernelGGL((moe_down_kernel<FMT, MODE, OutT, kW, kRt, 1, kCh, kAux>), grid, block, 0,
+                       stream, p, ws, groups);
+  };
+  if constexpr (FMT != kE2M1)           // e2m1: wide from 8 on
+    if (p.T * p.k > 8 * p.E) {
+      launch(std::integral_constant<int, 0>{});
+      return hipGetLastError();
+    }
+  launch(std::integral_constant<int, kNonTemporal>{});
   return hipGetLastError();
 }
 

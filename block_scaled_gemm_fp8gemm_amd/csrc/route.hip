@@ -42,7 +42,8 @@ __device__ __forceinline__ float key_logit(uint32_t key) {
   return __uint_as_float((key & 0x80000000u) ? (key & 0x7fffffffu) : ~key);
 }
 
-// L lanes per token, S experts per lane: L * S >= experts, k <= L.
+// L lanes per token, S experts per lane: L * S >= experts, k <= L.  Bound by latency: one row
+// of 8 logits 1.8 us, 4096 rows of 256, top-8, 6.9 us (8 rounds of 6 shuffles each).
 template <int L, int S>
 __global__ __launch_bounds__(kRouteThreads) void route_kernel(RouteProblem p) {
   constexpr int kPerBlock = kRouteThreads / L;
@@ -145,8 +146,8 @@ constexpr int kSortThreads = 1024;
 constexpr int kSortWaves = kSortThreads / 64;
 // One workgroup sorts up to 4096 positions alone; up to 64 blocks of 1024 a count kernel
 // and a placement kernel that adds the blocks before its own up; beyond, a kernel of prefix
-// sums between them.  (32768 positions of 8 groups: 13.0 us in three kernels of 4096
-// positions each.)
+// sums between them.  All bound by latency: 61 positions 3.6 us; 32768 of 8 groups 9.1 us
+// in two kernels, 13.0 in three (of 4096 positions a block).
 constexpr int kOneBlock = 4096;
 constexpr int kShortBlock = 1024, kShortBlocks = 64;
 constexpr int kLongBlock = 4096, kMaxBlocks = 256;
