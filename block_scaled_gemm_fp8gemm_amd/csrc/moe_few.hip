@@ -26,10 +26,10 @@
 // Both kernels are persistent: every workgroup derives the experts in use and their
 // slots from the ids, so the host never reads them.
 //
-// 8 experts of (4096, 14336), top-2, e4m3: one token 46 + 28 us for 235 and 117 MB of codes
-// (5.1 and 4.2 TB/s; a copy reaches 5.2, a plain stream of such tiles 6.7 to 7.0, the rest is
+// 8 experts of (4096, 14336), top-2, e4m3: one token 45 + 27 us for 235 and 117 MB of codes
+// (5.2 and 4.3 TB/s; a copy reaches 5.2, a plain stream of such tiles 6.7 to 7.0, the rest is
 // the start: lists, units and the first chunk's way from HBM, 5 us a kernel), 16 tokens
-// 141 + 81 us for 940 and 470 MB (6.7 and 5.8 TB/s).
+// 138 + 80 us for 940 and 470 MB (6.8 and 5.9 TB/s).
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -907,7 +907,8 @@ __global__ __launch_bounds__(64 * W, W / 4) void moe_down_kernel(MoeProblem p, W
 // CU draws from L2.  Here the waves of a workgroup split the rows instead of K: a unit is
 // 256 rows, 32 per wave, and the activations of a chunk are copied to LDS once for all of
 // them.  Three slots: while one chunk is multiplied, two are under way.  A wave keeps its
-// rows' sums to itself, so there is nothing to join.
+// rows' sums to itself, so there is nothing to join.  Bound by that lockstep, a barrier per
+// chunk: 4.7 TB/s of codes at best (16 tokens, 8 experts of (4096, 14336), e4m3).
 // ---------------------------------------------------------------------------
 template <int FMT, int MODE, int X, int NT>
 struct Wide {
@@ -1310,8 +1311,8 @@ int down_groups(int64_t H) { return (int)((H + 31) / 32); }
 // codes, whose activations are twice as many.  Narrow and wide, 8 experts of (4096, 14336),
 // top-2, both kernels' time in us (routing with a preference for some experts):
 //   pairs per expert     4          8         16         32
-//   e4m3              235 323    269 333    356 384    563 480
-//   e2m1              183 238    229 261    343 304    580 468
+//   e4m3              226 319    264 330    353 386    539 468
+//   e2m1              174 212    218 236    338 280    583 413
 template <int FMT>
 bool wide(int64_t T, int E, int k) {
   return T * k > (FMT == kE2M1 ? 8 : 16) * (int64_t)E;
